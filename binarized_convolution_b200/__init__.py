@@ -5,7 +5,9 @@ This package is a thin ctypes binding over ``libbconv.so`` (built in-tree by
 points (``bconv_create``, ``bconv_forward``, ``bfc_create``, ...) only marshal arguments;
 every step of the computation runs in the library's CUDA kernels.  PyTorch supplies device
 memory and the current CUDA stream in the convenience classes :class:`BinaryConv2d` and
-:class:`BinaryFC`.
+:class:`BinaryFC`, and for the operators around low-bit layers of a language model:
+:class:`QuantFC` (4-bit weights), :func:`block_norm` and :func:`token_logprobs` with their
+gradients.
 
 There is no CPU fallback: if the library is missing or no CUDA device is visible, the calls
 raise.
@@ -24,6 +26,9 @@ from ._native import (  # noqa: F401
     CTA_AUTO,
     CTA_PAIR,
     CTA_SINGLE,
+    DTYPE_BF16,
+    DTYPE_F16,
+    DTYPE_F32,
     STAGING_AUTO,
     STAGING_PER_TAP,
     STAGING_ROWS,
@@ -36,6 +41,10 @@ from ._native import (  # noqa: F401
     TYPE_BINARY_WEIGHTS,
     TYPE_XNOR,
     BconvError,
+    bconv_block_norm_backward,
+    bconv_block_norm_desc_t,
+    bconv_block_norm_forward,
+    bconv_block_norm_workspace_bytes,
     bconv_create,
     bconv_cta_mode,
     bconv_set_cta_mode,
@@ -68,6 +77,9 @@ from ._native import (  # noqa: F401
     bconv_set_algo,
     bconv_status_string,
     bconv_sync_status,
+    bconv_token_desc_t,
+    bconv_token_logprobs_backward,
+    bconv_token_logprobs_forward,
     bconv_version,
     bfc_create,
     bfc_cta_mode,
@@ -83,6 +95,14 @@ from ._native import (  # noqa: F401
     bfc_profile_begin,
     bfc_profile_end,
     bfc_profile_stride,
+    bfc_quant_create,
+    bfc_quant_desc_t,
+    bfc_quant_destroy,
+    bfc_quant_forward,
+    bfc_quant_input_feature_channels,
+    bfc_quant_output_feature_channels,
+    bfc_quant_sync_status,
+    bfc_quant_workspace_bytes,
     bfc_set_algo,
     bfc_sync_status,
     exported_symbols,
@@ -90,3 +110,18 @@ from ._native import (  # noqa: F401
     load_library,
 )
 from .layers import BinaryConv2d, BinaryFC  # noqa: F401
+
+
+_LM_OPS = ("QuantFC", "BlockNorm", "BlockNormGrad", "TokenLogprobs", "block_norm", "block_norm_backward",
+           "token_logprobs", "token_logprobs_backward")
+
+
+def __getattr__(name):
+    # (the module of these needs torch at import; the C binding above does not)
+    if name in _LM_OPS:
+        from . import lm_ops
+
+        for n in _LM_OPS:
+            globals()[n] = getattr(lm_ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

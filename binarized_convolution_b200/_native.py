@@ -27,6 +27,7 @@ ALGO_AUTO, ALGO_POPC, ALGO_SIMT_F32, ALGO_TCGEN05 = 0, 1, 2, 3
 CTA_AUTO, CTA_SINGLE, CTA_PAIR = 0, 1, 2
 CODES_AUTO, CODES_INT8, CODES_FP4, CODES_BF16X3 = 0, 1, 2, 3
 STAGING_AUTO, STAGING_PER_TAP, STAGING_ROWS, STAGING_INPUT = 0, 1, 2, 3
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 
 _STATUS = {0: "BCONV_OK", 1: "BCONV_ERR_INVALID_ARG", 2: "BCONV_ERR_UNSUPPORTED", 3: "BCONV_ERR_CUDA",
            4: "BCONV_ERR_OOM", 5: "BCONV_ERR_TIMEOUT", 6: "BCONV_ERR_NO_DEVICE"}
@@ -53,10 +54,26 @@ class bconv_io_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("in_", "in_bits", "in_a", "out", "out_bits", "out_a")]
 
 
+class bfc_quant_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_channels", "out_channels", "group_size", "neuron", "in_dtype",
+                                              "out_dtype")]
+
+
+class bconv_block_norm_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class bconv_token_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("stride", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("top", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _SIGS = {
     "bconv_create": (_I32, [ctypes.POINTER(bconv_desc_t), _P, _P, _P, _P, _P, _I32, ctypes.c_uint32, ctypes.POINTER(_P)]),
     "bconv_forward": (_I32, [_P, _P, _P, _P]),
@@ -103,6 +120,18 @@ _SIGS = {
     "bconv_set_staging": (_I32, [_I32]),
     "bconv_staging": (_I32, [_P]),
     "bfc_tc_codes": (_I32, [_P]),
+    "bfc_quant_create": (_I32, [ctypes.POINTER(bfc_quant_desc_t), _P, _P, _P, _P, ctypes.POINTER(_P)]),
+    "bfc_quant_workspace_bytes": (_I64, [_P, _I64]),
+    "bfc_quant_forward": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "bfc_quant_input_feature_channels": (_I32, [_P]),
+    "bfc_quant_output_feature_channels": (_I32, [_P]),
+    "bfc_quant_sync_status": (_I32, [_P, _P]),
+    "bfc_quant_destroy": (_I32, [_P]),
+    "bconv_block_norm_forward": (_I32, [ctypes.POINTER(bconv_block_norm_desc_t)] + [_P] * 8),
+    "bconv_block_norm_workspace_bytes": (_I64, [ctypes.POINTER(bconv_block_norm_desc_t)]),
+    "bconv_block_norm_backward": (_I32, [ctypes.POINTER(bconv_block_norm_desc_t)] + [_P] * 14),
+    "bconv_token_logprobs_forward": (_I32, [ctypes.POINTER(bconv_token_desc_t)] + [_P] * 8),
+    "bconv_token_logprobs_backward": (_I32, [ctypes.POINTER(bconv_token_desc_t)] + [_P] * 7 + [_I64, _P]),
 }
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -402,3 +431,83 @@ def bconv_forward_noalloc(desc: bconv_desc_t, type: int, flags: int, weights_ptr
     _check(load_library().bconv_forward_noalloc(ctypes.byref(desc), int(type), int(flags), weights_ptr, scale_ptr,
                                                 bias_ptr, in_scale_ptr, in_bias_ptr, in_ptr, out_ptr, stream),
            "bconv_forward_noalloc")
+
+
+def bfc_quant_create(desc: bfc_quant_desc_t, codes_ptr: int, scale_ptr: int, zero_ptr: int | None = None,
+                     bias_ptr: int | None = None):
+    """A 4-bit fully-connected layer from host or device arrays (addresses); returns its handle."""
+    h = _P()
+    _check(load_library().bfc_quant_create(ctypes.byref(desc), codes_ptr, scale_ptr, zero_ptr, bias_ptr,
+                                           ctypes.byref(h)), "bfc_quant_create")
+    return h
+
+
+def bfc_quant_workspace_bytes(h, rows: int) -> int:
+    return load_library().bfc_quant_workspace_bytes(h, int(rows))
+
+
+def bfc_quant_forward(h, in_ptr: int, in_stride: int, rows: int, out_ptr: int, out_stride: int,
+                      workspace_ptr: int | None = None, stream: int = 0):
+    st = load_library().bfc_quant_forward(h, in_ptr, in_stride, rows, out_ptr, out_stride, workspace_ptr, stream)
+    if st:
+        raise BconvError(st, "bfc_quant_forward")
+
+
+def bfc_quant_input_feature_channels(h) -> int:
+    return load_library().bfc_quant_input_feature_channels(h)
+
+
+def bfc_quant_output_feature_channels(h) -> int:
+    return load_library().bfc_quant_output_feature_channels(h)
+
+
+def bfc_quant_sync_status(h, stream: int = 0):
+    _check(load_library().bfc_quant_sync_status(h, stream), "bfc_quant_sync_status")
+
+
+def bfc_quant_destroy(h):
+    if h is not None:
+        _check(load_library().bfc_quant_destroy(h), "bfc_quant_destroy")
+
+
+def bconv_block_norm_forward(desc: bconv_block_norm_desc_t, residual_ptr, block_ptr, gate_ptr, post_weight_ptr,
+                             pre_weight_ptr, residual_out_ptr, normed_ptr, stream: int = 0):
+    """Device addresses (or None); see include/bconv.h."""
+    st = load_library().bconv_block_norm_forward(desc, residual_ptr, block_ptr, gate_ptr, post_weight_ptr,
+                                                 pre_weight_ptr, residual_out_ptr, normed_ptr, stream)
+    if st:
+        raise BconvError(st, "bconv_block_norm_forward")
+
+
+def bconv_block_norm_workspace_bytes(desc: bconv_block_norm_desc_t) -> int:
+    return load_library().bconv_block_norm_workspace_bytes(desc)
+
+
+def bconv_block_norm_backward(desc: bconv_block_norm_desc_t, residual_out_ptr, block_ptr, gate_ptr, post_weight_ptr,
+                              pre_weight_ptr, d_residual_out_ptr, d_normed_ptr, d_residual_ptr, d_block_ptr,
+                              d_pre_weight_ptr, d_post_weight_ptr, d_gate_ptr, workspace_ptr, stream: int = 0):
+    """Device addresses (or None); see include/bconv.h."""
+    st = load_library().bconv_block_norm_backward(desc, residual_out_ptr, block_ptr, gate_ptr, post_weight_ptr,
+                                                  pre_weight_ptr, d_residual_out_ptr, d_normed_ptr, d_residual_ptr,
+                                                  d_block_ptr, d_pre_weight_ptr, d_post_weight_ptr, d_gate_ptr,
+                                                  workspace_ptr, stream)
+    if st:
+        raise BconvError(st, "bconv_block_norm_backward")
+
+
+def bconv_token_logprobs_forward(desc: bconv_token_desc_t, logits_ptr, tokens_ptr, logprob_ptr, entropy_ptr, lse_ptr,
+                                 top_logprob_ptr, top_index_ptr, stream: int = 0):
+    """Device addresses (or None); see include/bconv.h."""
+    st = load_library().bconv_token_logprobs_forward(desc, logits_ptr, tokens_ptr, logprob_ptr, entropy_ptr, lse_ptr,
+                                                     top_logprob_ptr, top_index_ptr, stream)
+    if st:
+        raise BconvError(st, "bconv_token_logprobs_forward")
+
+
+def bconv_token_logprobs_backward(desc: bconv_token_desc_t, logits_ptr, tokens_ptr, lse_ptr, entropy_ptr,
+                                  d_logprob_ptr, d_entropy_ptr, d_logits_ptr, d_stride: int, stream: int = 0):
+    """Device addresses (or None); see include/bconv.h."""
+    st = load_library().bconv_token_logprobs_backward(desc, logits_ptr, tokens_ptr, lse_ptr, entropy_ptr,
+                                                      d_logprob_ptr, d_entropy_ptr, d_logits_ptr, d_stride, stream)
+    if st:
+        raise BconvError(st, "bconv_token_logprobs_backward")

@@ -21,6 +21,7 @@
 
 #include "bconv.h"
 #include "common.cuh"
+#include "host_util.cuh"
 #include "tc_conv.cuh"
 
 namespace bconv {
@@ -37,22 +38,6 @@ int current_sm_count() {
 }
 
 namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) {
-      ok = false;
-      return;
-    }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 // Device allocations owned by a handle, freed together.
 struct DevMem {
@@ -94,13 +79,6 @@ struct Profile {
     active = false;
   }
 };
-
-bconv_status_t from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return BCONV_OK;
-  if (e == cudaErrorMemoryAllocation) return BCONV_ERR_OOM;
-  if (e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver) return BCONV_ERR_NO_DEVICE;
-  return BCONV_ERR_CUDA;
-}
 
 // Everything both handle kinds share: parameters on the device, workspace, settings.
 struct Layer {

@@ -1,0 +1,502 @@
+// What rows of logits say (bconv_token_logprobs_*): log-sum-exp, entropy, the log probability of
+// a given token and the top alternatives in one pass over the logits, and the gradient of log
+// probability and entropy in another.
+//
+// With x = logits / temperature and m the largest logit seen, each thread keeps
+//     s = sum exp((l - m) / temperature)     t = sum exp((l - m) / temperature) (l - m) / temperature
+// over its elements (rescaled when m grows), and these join pairwise, so a row is read once:
+//     lse = m / temperature + log s          entropy = log s - t / s
+// Differences to m are taken before the scale, so logits of the type's lowest value (masks) stay
+// finite, and log probabilities are (l - m) / temperature - log s, exact where l is near m.
+//
+// Top alternatives: the k-th largest of the maxima of disjoint groups of elements is a lower
+// bound of the k-th largest element.  After a CTA's first elements it takes that bound from its
+// threads' maxima and from then on only collects elements that reach it (few, unless the row is
+// sorted); the collected ones are ordered by counting for each how many come before it.  If more
+// are found than the buffer holds (long runs of equal logits, sorted rows), a second pass uses the bound
+// of the whole row, and if that does not suffice either, k passes over the row pick one each.
+// Every path gives the same answer: logits in descending order, equal ones by index.
+//
+// A row is one CTA's work, or a cluster's where there are few rows; the cluster's CTAs hand their (m, s,
+// t) and their own top k to the first one through its shared memory.
+//
+// Bound by HBM (one read of the logits; in the gradient one read and one write).
+#include <float.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "dtype.cuh"
+#include "host_util.cuh"
+#include "tc_device.cuh"
+
+namespace bconv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMaxTop = 64;
+constexpr int kCap = 1024;       // collected elements of one CTA
+constexpr int kGroups = 128;     // groups of 4 threads whose maxima bound the k-th largest
+constexpr int kMaxCluster = 8;
+constexpr float kFar = -1e4f;    // exp of it and of anything below is 0; keeps 0 * d finite
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// 2^x by the hardware's approximation (relative error below 2^-22; -inf gives 0)
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Order-preserving integer of a logit: larger values give larger keys, +-0 the same one, NaN the
+// largest.  Keys are above 0, so 0 stands for "nothing".
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (k == 0xffffffffu) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// (key, index) as one number that grows with the key and, for equal keys, falls with the index
+__device__ __forceinline__ unsigned long long entry(uint32_t key, uint32_t index) {
+  return (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - index);
+}
+__device__ __forceinline__ uint32_t entry_index(unsigned long long e) { return 0xffffffffu - static_cast<uint32_t>(e); }
+
+struct Stat {
+  float m, s, t;  // s and t relative to the largest logit m, in units of 1 / temperature
+};
+
+// The same relative to a larger m (scale = 1 / temperature).
+__device__ __forceinline__ void raise(Stat& a, float m, float scale) {
+  if (m > a.m) {
+    // with nothing but -inf so far s and t are 0 (or NaN, which stays)
+    const float d = a.m == -INFINITY ? -FLT_MAX : (a.m - m) * scale;
+    const float f = exp2_approx(d * kLog2e);
+    a.t = fmaf(a.s, fmaxf(d, kFar), a.t) * f;
+    a.s *= f;
+    a.m = m;
+  }
+}
+__device__ __forceinline__ Stat join(Stat a, Stat b, float scale) {
+  raise(a, b.m, scale);
+  raise(b, a.m, scale);
+  return {a.m, a.s + b.s, a.t + b.t};
+}
+
+struct FwdArgs {
+  const void* logits;
+  const int64_t* tokens;
+  float *logprob, *entropy, *lse, *top_logprob;
+  int32_t* top_index;
+  int64_t rows, stride;
+  int vocab, top;
+  float scale;  // 1 / temperature
+};
+
+struct Shared {
+  Stat stat[kThreads / 32];
+  Stat peers[kMaxCluster];                                  // first CTA: every CTA's statistics
+  unsigned long long top[kMaxCluster * kMaxTop];            // first CTA: every CTA's top entries
+  unsigned long long best[kThreads / 32];                   // one round of the slow selection
+  unsigned long long found[kCap];
+  uint32_t group[kGroups];
+  uint32_t bound;
+  int count;
+};
+
+// Element range [begin, end) of a row for a thread's loop: f(index, value) once for each element,
+// 8 at a time from 16-byte aligned addresses, the ragged ends one at a time.
+template <typename T, typename F8, typename F1>
+__device__ __forceinline__ void each(const T* row, int begin, int end, F8&& f8, F1&& f1) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + begin);
+  int head = static_cast<int>(((16 - (at & 15u)) & 15u) / sizeof(T));
+  head = min(head, end - begin);
+  const int body = (end - begin - head) / 8;
+  const int tail = begin + head + body * 8;
+  if (static_cast<int>(threadIdx.x) < head) f1(begin + threadIdx.x, to_f32(row[begin + threadIdx.x]));
+  for (int i = threadIdx.x; i < body; i += kThreads) {
+    Raw8<T> w;
+    const int c = begin + head + i * 8;
+    w.load(row + c);
+    float v[8];
+    w.unpack(v);
+    f8(c, v);
+  }
+  if (tail + static_cast<int>(threadIdx.x) < end) f1(tail + threadIdx.x, to_f32(row[tail + threadIdx.x]));
+}
+
+// The `top`-th largest of the maxima of the CTA's groups of 4 threads, as a key (0 while
+// fewer groups have seen an element).  `mx`: this thread's largest key, 0 for none.
+__device__ __forceinline__ uint32_t bound_of(Shared& S, uint32_t mx, int top) {
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  if ((threadIdx.x & 3) == 0) S.group[threadIdx.x >> 2] = mx;
+  if (threadIdx.x == 0) S.bound = 0;
+  __syncthreads();
+  if (threadIdx.x < kGroups) {
+    const uint32_t own = S.group[threadIdx.x];
+    int before = 0;
+    for (int i = 0; i < kGroups; ++i) {
+      const uint32_t o = S.group[i];
+      before += o > own || (o == own && i < static_cast<int>(threadIdx.x));
+    }
+    if (before == top - 1) S.bound = own;  // exactly one thread
+  }
+  __syncthreads();
+  return S.bound;
+}
+
+__device__ __forceinline__ void collect(Shared& S, uint32_t key, int index) {
+  const int at = atomicAdd(&S.count, 1);
+  if (at < kCap) S.found[at] = entry(key, static_cast<uint32_t>(index));
+}
+
+// The largest `top` of n entries (distinct), in order, to out[0 .. top): counts for each how many come before.
+__device__ __forceinline__ void order_entries(const unsigned long long* from, int n, int top, unsigned long long* out) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const unsigned long long own = from[i];
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += from[j] > own;
+    if (before < top) out[before] = own;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdArgs a) {
+  __shared__ Shared S;
+  uint32_t rank, peers;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(peers));
+  const int64_t r = blockIdx.x / peers;
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  // this CTA's part of the row: whole 8-element steps
+  const int part = static_cast<int>(((static_cast<int64_t>(a.vocab) + peers - 1) / peers + 7) / 8 * 8);
+  const int begin = static_cast<int>(min(static_cast<int64_t>(rank) * part, static_cast<int64_t>(a.vocab)));
+  const int end = static_cast<int>(min(static_cast<int64_t>(begin) + part, static_cast<int64_t>(a.vocab)));
+  const int top = min(a.top, end - begin);  // this part's share of the candidates
+  const float scale = a.scale;
+  if (threadIdx.x == 0) S.count = 0;
+  // (awaited before the first access to another CTA's shared memory: that CTA has started by then)
+  if (peers > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+  // first elements, for the bound on the top entries
+  uint32_t bound = 0;
+  if (top > 0) {
+    uint32_t mx = 0;
+    const int first = min(end, begin + kThreads * 8 + 16);
+    each(row, begin, first,
+         [&](int, const float (&v)[8]) {
+#pragma unroll
+           for (int e = 0; e < 8; ++e) mx = max(mx, order_key(v[e]));
+         },
+         [&](int, float v) { mx = max(mx, order_key(v)); });
+    bound = bound_of(S, mx, top);
+  }
+  __syncthreads();
+
+  Stat st = {-INFINITY, 0.f, 0.f};
+  const bool want = top > 0;
+  const float bound_value = bound ? key_value(bound) : -INFINITY;  // (NaN: only NaNs reach it)
+  auto add = [&](float v) {
+    const float d = v == -INFINITY ? -FLT_MAX : (v - st.m) * scale;  // (v <= m here, or NaN)
+    const float e = exp2_approx(d * kLog2e);
+    st.s += e;
+    st.t = fmaf(e, fmaxf(d, kFar), st.t);
+  };
+  each(row, begin, end,
+       [&](int c, const float (&v)[8]) {
+         float mx = v[0];
+         bool nan = v[0] != v[0];
+#pragma unroll
+         for (int e = 1; e < 8; ++e) {
+           mx = fmaxf(mx, v[e]);
+           nan |= v[e] != v[e];
+         }
+         raise(st, mx, scale);
+#pragma unroll
+         for (int e = 0; e < 8; ++e) add(v[e]);
+         if (want && (!(mx < bound_value) || nan))
+#pragma unroll
+           for (int e = 0; e < 8; ++e) {
+             const uint32_t k = order_key(v[e]);
+             if (k >= bound) collect(S, k, c + e);
+           }
+       },
+       [&](int c, float v) {
+         raise(st, v, scale);
+         add(v);
+         if (want) {
+           const uint32_t k = order_key(v);
+           if (k >= bound) collect(S, k, c);
+         }
+       });
+
+  // statistics of the CTA
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat b;
+    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+    st = join(st, b, scale);
+  }
+  if ((threadIdx.x & 31) == 0) S.stat[threadIdx.x >> 5] = st;
+  __syncthreads();
+
+  // this part's top entries, in order, into the first CTA's shared memory
+  if (want) {
+    int n = S.count;
+    unsigned long long* mine = S.top;
+    if (n > kCap) {  // uniform: the bound of the whole part
+      uint32_t mx = 0;
+      each(row, begin, end,
+           [&](int, const float (&v)[8]) {
+#pragma unroll
+             for (int e = 0; e < 8; ++e) mx = max(mx, order_key(v[e]));
+           },
+           [&](int, float v) { mx = max(mx, order_key(v)); });
+      __syncthreads();
+      if (threadIdx.x == 0) S.count = 0;
+      bound = bound_of(S, mx, top);
+      each(row, begin, end,
+           [&](int c, const float (&v)[8]) {
+#pragma unroll
+             for (int e = 0; e < 8; ++e) {
+               const uint32_t k = order_key(v[e]);
+               if (k >= bound) collect(S, k, c + e);
+             }
+           },
+           [&](int c, float v) {
+             const uint32_t k = order_key(v);
+             if (k >= bound) collect(S, k, c);
+           });
+      __syncthreads();
+      n = S.count;
+    }
+    if (n <= kCap) {
+      order_entries(S.found, n, top, mine);
+    } else {  // one pass per entry: the largest below the last one
+      unsigned long long last = ~0ull;
+      for (int i = 0; i < top; ++i) {
+        unsigned long long best = 0;
+        each(row, begin, end,
+             [&](int c, const float (&v)[8]) {
+#pragma unroll
+               for (int e = 0; e < 8; ++e) {
+                 const unsigned long long x = entry(order_key(v[e]), static_cast<uint32_t>(c + e));
+                 if (x < last && x > best) best = x;
+               }
+             },
+             [&](int c, float v) {
+               const unsigned long long x = entry(order_key(v), static_cast<uint32_t>(c));
+               if (x < last && x > best) best = x;
+             });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if ((threadIdx.x & 31) == 0) S.best[threadIdx.x >> 5] = best;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w) best = max(best, S.best[w]);
+        __syncthreads();
+        if (threadIdx.x == 0) mine[i] = best;
+        last = best;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    st = S.stat[0];
+    for (int w = 1; w < kThreads / 32; ++w) st = join(st, S.stat[w], scale);
+  }
+  __syncthreads();
+  int n = top;
+  if (peers > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // every CTA's result to the first one (whose own entries are in place: peer p's start at p * a.top)
+    if (rank != 0) {
+      const uint32_t to = tcdev::mapa(&S.top[rank * a.top], 0), stat = tcdev::mapa(&S.peers[rank], 0);
+      for (int i = threadIdx.x; i < a.top; i += kThreads) {
+        const unsigned long long v = i < top ? S.top[i] : 0ull;
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8u * i), "l"(v) : "memory");
+      }
+      if (threadIdx.x == 0) {
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(stat), "f"(st.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(stat + 4u), "f"(st.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(stat + 8u), "f"(st.t) : "memory");
+      }
+    }
+    __syncwarp();
+    tcdev::cluster_sync();
+    if (rank != 0) return;
+    if (threadIdx.x == 0)
+      for (uint32_t p = 1; p < peers; ++p) st = join(st, S.peers[p], scale);
+    if (a.top > 0) {
+      // entries of 0 ("nothing") come last: there are at least a.top real ones
+      for (int i = threadIdx.x; i < static_cast<int>(peers) * a.top; i += kThreads) S.found[i] = i < a.top && i >= top ? 0ull : S.top[i];
+      __syncthreads();
+      order_entries(S.found, static_cast<int>(peers) * a.top, a.top, S.top);
+    }
+    n = a.top;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) S.stat[0] = st;
+  __syncthreads();
+  st = S.stat[0];
+  const bool nothing = st.m == -INFINITY && st.s == 0.f;
+  const float log_s = __log2f(st.s) * kLn2;
+  auto logprob = [&](float v) {
+    if (nothing || v == -INFINITY) return st.s != st.s ? st.s : -INFINITY;
+    return (v - st.m) * scale - log_s;
+  };
+  if (threadIdx.x == 0) {
+    if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(st.m, scale, log_s);
+    if (a.entropy) a.entropy[r] = nothing ? 0.f : log_s - st.t / st.s;
+    if (a.logprob) {
+      const int64_t token = a.tokens[r];
+      a.logprob[r] = token < 0 ? 0.f : token >= a.vocab ? __uint_as_float(0x7fc00000u) : logprob(to_f32(row[token]));
+    }
+  }
+  if (a.top_index && static_cast<int>(threadIdx.x) < n) {
+    const unsigned long long x = S.top[threadIdx.x];
+    a.top_index[r * a.top + threadIdx.x] = static_cast<int32_t>(entry_index(x));
+    a.top_logprob[r * a.top + threadIdx.x] = logprob(key_value(static_cast<uint32_t>(x >> 32)));
+  }
+}
+
+struct BwdArgs {
+  const void* logits;
+  const int64_t* tokens;
+  const float *lse, *entropy, *d_logprob, *d_entropy;
+  void* d_logits;
+  int64_t rows, stride, d_stride;
+  int vocab, parts;  // CTAs per row
+  float scale;
+};
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdStep = kBwdThreads * 8 * 4;  // elements of one CTA
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const BwdArgs a) {
+  const int64_t r = blockIdx.x / a.parts;
+  const int begin = static_cast<int>(blockIdx.x - r * a.parts) * kBwdStep;
+  const int end = min(a.vocab, begin + kBwdStep);
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  T* to = static_cast<T*>(a.d_logits) + r * a.d_stride;
+  const float lse = a.lse[r], h = a.d_entropy ? a.entropy[r] : 0.f;
+  const int64_t token = a.d_logprob ? a.tokens[r] : -1;
+  float g = 0.f;
+  if (token >= 0) g = token < a.vocab ? a.d_logprob[r] : __uint_as_float(0x7fc00000u);
+  const float ge = a.d_entropy ? a.d_entropy[r] : 0.f;
+  const float scale = a.scale;
+  auto grad = [&](int c, float v) {
+    // -inf: probability 0 (in a row of nothing else too)
+    const float logp = v == -INFINITY ? -INFINITY : fmaf(v, scale, -lse);
+    const float p = exp2_approx(logp * kLog2e);
+    float d = -p * (g + (p == 0.f ? 0.f : ge * (logp + h)));
+    if (c == token) d += g;
+    return d * scale;
+  };
+  const bool vec = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(to)) & 15u) == 0;
+  if (vec) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + begin);
+    const int head = min(end - begin, static_cast<int>(((16 - (at & 15u)) & 15u) / sizeof(T)));
+    const int body = (end - begin - head) / 8, tail = begin + head + body * 8;
+    if (static_cast<int>(threadIdx.x) < head) {
+      const int c = begin + threadIdx.x;
+      to[c] = from_f32<T>(grad(c, to_f32(row[c])));
+    }
+    for (int i = threadIdx.x; i < body; i += kBwdThreads) {
+      const int c = begin + head + i * 8;
+      Raw8<T> w;
+      w.load(row + c);
+      float v[8];
+      w.unpack(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = grad(c + e, v[e]);
+      w.pack(v);
+      w.store(to + c);
+    }
+    if (tail + static_cast<int>(threadIdx.x) < end) {
+      const int c = tail + threadIdx.x;
+      to[c] = from_f32<T>(grad(c, to_f32(row[c])));
+    }
+  } else {
+    for (int c = begin + threadIdx.x; c < end; c += kBwdThreads) to[c] = from_f32<T>(grad(c, to_f32(row[c])));
+  }
+}
+
+bconv_status_t check_desc(const bconv_token_desc_t* d) {
+  if (!d || d->rows < 0 || d->rows > (int64_t{1} << 28) || d->vocab < 1 || d->vocab > (1 << 30) || d->stride < d->vocab ||
+      !valid_dtype(d->dtype) || !(d->temperature > 0.f) || d->temperature > FLT_MAX || 1.f / d->temperature > FLT_MAX)
+    return BCONV_ERR_INVALID_ARG;
+  return BCONV_OK;
+}
+
+template <typename T>
+cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
+  // few rows: a cluster per row, as long as every CTA keeps a few thousand elements
+  const int sms = current_sm_count();
+  unsigned peers = 1;
+  while (peers < kMaxCluster && a.rows * peers * 2 <= 2 * sms && a.vocab / static_cast<int>(peers) >= 4 * kThreads) peers *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * peers);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = peers;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs_fwd_kernel<T>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace bconv
+
+using namespace bconv;
+
+extern "C" {
+
+bconv_status_t bconv_token_logprobs_forward(const bconv_token_desc_t* d, const void* logits, const int64_t* tokens,
+                                            float* logprob, float* entropy, float* lse, float* top_logprob,
+                                            int32_t* top_index, struct CUstream_st* stream) {
+  const bconv_status_t st = check_desc(d);
+  if (st != BCONV_OK) return st;
+  if (d->top < 0 || d->top > kMaxTop || d->top > d->vocab || (logprob && !tokens) || !aligned_elem(logits, d->dtype))
+    return BCONV_ERR_INVALID_ARG;
+  if (d->rows == 0) return BCONV_OK;
+  if (!logits || (d->top > 0) != (top_logprob != nullptr) || (d->top > 0) != (top_index != nullptr))
+    return BCONV_ERR_INVALID_ARG;
+  FwdArgs a{logits, tokens, logprob, entropy, lse, top_logprob, top_index, d->rows, d->stride, d->vocab, d->top,
+            1.f / d->temperature};
+  return from_cuda(with_dtype(d->dtype, [&](auto t) { return launch_fwd<decltype(t)>(a, stream); }));
+}
+
+bconv_status_t bconv_token_logprobs_backward(const bconv_token_desc_t* d, const void* logits,
+                                             const int64_t* tokens, const float* lse, const float* entropy,
+                                             const float* d_logprob, const float* d_entropy, void* d_logits,
+                                             int64_t d_stride, struct CUstream_st* stream) {
+  const bconv_status_t st = check_desc(d);
+  if (st != BCONV_OK) return st;
+  if (d_stride < d->vocab || (d_logprob && !tokens) || (d_entropy && !entropy) || !aligned_elem(logits, d->dtype) ||
+      !aligned_elem(d_logits, d->dtype) || (logits && logits == d_logits && d_stride != d->stride))
+    return BCONV_ERR_INVALID_ARG;
+  if (d->rows == 0) return BCONV_OK;
+  if (!logits || !lse || !d_logits) return BCONV_ERR_INVALID_ARG;
+  BwdArgs a{logits, tokens, lse, entropy, d_logprob, d_entropy, d_logits, d->rows, d->stride, d_stride, d->vocab,
+            static_cast<int>(ceil_div(d->vocab, kBwdStep)), 1.f / d->temperature};
+  const int64_t ctas = a.rows * a.parts;
+  if (ctas > 0x7fffffff) return BCONV_ERR_UNSUPPORTED;
+  return from_cuda(with_dtype(d->dtype, [&](auto t) {
+    token_logprobs_bwd_kernel<decltype(t)><<<static_cast<unsigned>(ctas), kBwdThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }));
+}
+
+}  // extern "C"

@@ -1,0 +1,356 @@
+"""The operators of a language model around its low-bit layers, on torch CUDA tensors.
+
+:class:`QuantFC` is a layer object like the binary ones; :func:`block_norm` and
+:func:`token_logprobs` (and their ``_backward``) are functions.  They only marshal: they check
+types, shapes and devices, allocate outputs and workspaces with torch and call the C entry points on
+the current stream of the tensors' device.  Activations are float32, bfloat16 or float16; inputs
+whose last dimension (or, where rows have to be packed, whose rows) are not contiguous are
+copied.  Gradients are explicit calls; nothing here records for autograd.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import ctypes
+import torch
+
+from . import _native as nat
+from .layers import _Layer
+
+_DTYPES = {torch.float32: nat.DTYPE_F32, torch.bfloat16: nat.DTYPE_BF16, torch.float16: nat.DTYPE_F16}
+_NAMED = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _dtype(t) -> torch.dtype:
+    t = _NAMED.get(t, t)
+    if t not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {t}")
+    return t
+
+
+def _on(x):
+    """A context that makes x's device current (nothing to do, and nothing spent, when it is)."""
+    return torch.cuda.device(x.device)
+
+
+def _stream(x) -> int:
+    return torch._C._cuda_getCurrentRawStream(x.device.index)
+
+
+def _is_current(x) -> bool:
+    return x.device.index == torch.cuda.current_device()
+
+
+def _activation(x, name):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {x.dtype}")
+    return x
+
+
+def _like(t, ref, shape, name, dtype=None):
+    """t as a contiguous tensor, checked against ref's device, the dtype and the shape; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != ref.device:
+        raise TypeError(f"{name}: expected a tensor on {ref.device}")
+    if t.dtype != (dtype or ref.dtype):
+        raise TypeError(f"{name}: expected {dtype or ref.dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.contiguous()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(x):
+    """(tensor, rows, row stride) of x as a matrix over its last dimension; copied if it is none."""
+    if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]:
+        return x, x.shape[0], x.stride(0)
+    x = x.contiguous()
+    width = x.shape[-1]
+    return x, x.numel() // width if width else 0, width
+
+
+class QuantFC(_Layer):
+    """A fully-connected layer with 4-bit weights and group scales on the current CUDA device.
+
+    ``W[c][f] = scale[c][f // group_size] * (code[c][f] - zero[c][f // group_size])``.
+
+    codes: uint8 0..15 [out_channels, in_channels], or ``packed`` uint8 [out_channels,
+    ceil(in_channels / 2)], channel f in the low (f even) or high four bits of byte f // 2.  scale: float32
+    [out_channels, groups]; zero: uint8 of the same shape (None: 8); bias: float32 [out_channels].  All
+    may be numpy arrays or torch tensors on the host or the device; they are copied.
+    group_size: 32, 64, a multiple of 128, or at least in_channels.
+
+    ``layer(x)`` takes [..., in_channels] of ``dtype`` and returns [..., out_channels] of
+    ``out_dtype`` (default: dtype).  A layer may be used on several streams at once.
+    """
+
+    _destroy = staticmethod(nat.bfc_quant_destroy)
+
+    def __init__(self, in_channels, out_channels, *, codes=None, packed=None, scale, zero=None, bias=None,
+                 group_size=128, relu=False, dtype=torch.bfloat16, out_dtype=None):
+        self.handle = None
+        self.in_channels, self.out_channels = int(in_channels), int(out_channels)
+        self.dtype = _dtype(dtype)
+        self.out_dtype = _dtype(out_dtype) if out_dtype is not None else self.dtype
+        if group_size < 1 or in_channels < 1 or out_channels < 1:
+            raise ValueError("in_channels, out_channels and group_size must be positive")
+        groups = -(-self.in_channels // group_size)
+        if packed is None:
+            if codes is None:
+                raise ValueError("give codes or packed")
+            packed = self.pack(self._array(codes, torch.uint8, (self.out_channels, self.in_channels), "codes"))
+        packed = self._array(packed, torch.uint8, (self.out_channels, (self.in_channels + 1) // 2), "packed")
+        scale = self._array(scale, torch.float32, (self.out_channels, groups), "scale")
+        zero = self._array(zero, torch.uint8, (self.out_channels, groups), "zero")
+        bias = self._array(bias, torch.float32, (self.out_channels,), "bias")
+        for t in (packed, scale, zero, bias):
+            if t is not None and t.is_cuda:
+                torch.cuda.current_stream(t.device).synchronize()  # the layout kernels run on another stream
+        desc = nat.bfc_quant_desc_t(self.in_channels, self.out_channels, int(group_size),
+                                    nat.NEURON_RELU if relu else nat.NEURON_NONE, _DTYPES[self.dtype],
+                                    _DTYPES[self.out_dtype])
+        self.handle = nat.bfc_quant_create(desc, _ptr(packed), _ptr(scale), _ptr(zero), _ptr(bias))
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    @staticmethod
+    def _array(a, dtype, shape, name):
+        if a is None:
+            return None
+        t = torch.as_tensor(a)
+        if t.dtype != dtype:
+            if dtype == torch.uint8 or not t.dtype.is_floating_point:
+                raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+            t = t.to(dtype)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        return t.contiguous()
+
+    @staticmethod
+    def pack(codes):
+        """uint8 codes [..., n] -> packed uint8 [..., ceil(n / 2)]."""
+        codes = torch.as_tensor(codes) & 15
+        if codes.shape[-1] % 2:
+            codes = torch.nn.functional.pad(codes, (0, 1))
+        return codes[..., 0::2] | (codes[..., 1::2] << 4)
+
+    @property
+    def input_feature_channels(self) -> int:
+        return nat.bfc_quant_input_feature_channels(self.handle)
+
+    @property
+    def output_feature_channels(self) -> int:
+        return nat.bfc_quant_output_feature_channels(self.handle)
+
+    def forward_into(self, x, out):
+        """x [..., in_channels] into out [..., out_channels] (the rows of out may be strided)."""
+        if self.handle is None:
+            raise ValueError("the layer is closed")
+        if not isinstance(x, torch.Tensor) or x.device != self.device or out.device != self.device:
+            raise TypeError(f"expected tensors on {self.device}")
+        if x.dtype != self.dtype or out.dtype != self.out_dtype:
+            raise TypeError(f"expected {self.dtype} -> {self.out_dtype}, got {x.dtype} -> {out.dtype}")
+        if x.shape[-1] != self.in_channels or out.shape != x.shape[:-1] + (self.out_channels,):
+            raise ValueError(f"expected [..., {self.in_channels}] -> [..., {self.out_channels}], got "
+                             f"{tuple(x.shape)} -> {tuple(out.shape)}")
+        x, rows, in_stride = _rows(x)
+        to, _, out_stride = _rows(out)
+        if to.data_ptr() != out.data_ptr():
+            raise ValueError("out must have contiguous channels, and rows without gaps unless it is a matrix")
+        need = nat.bfc_quant_workspace_bytes(self.handle, rows)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need > 0 else None
+        nat.bfc_quant_forward(self.handle, x.data_ptr(), in_stride, rows, to.data_ptr(), out_stride, _ptr(ws),
+                              _stream(x))
+        return out
+
+    def __call__(self, x):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError("expected a CUDA tensor")
+        if x.dim() < 1:
+            raise ValueError("expected [..., in_channels]")
+        out = torch.empty(x.shape[:-1] + (self.out_channels,), dtype=self.out_dtype, device=x.device)
+        return self.forward_into(x, out)
+
+    def sync_status(self):
+        with torch.cuda.device(self.device):
+            nat.bfc_quant_sync_status(self.handle, _stream_of(self.device))
+
+
+def _stream_of(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class BlockNorm(NamedTuple):
+    residual_out: torch.Tensor
+    normed: torch.Tensor | None
+
+
+class BlockNormGrad(NamedTuple):
+    d_residual: torch.Tensor
+    d_block: torch.Tensor | None
+    d_pre_weight: torch.Tensor | None
+    d_post_weight: torch.Tensor | None
+    d_gate: torch.Tensor | None
+
+
+def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps):
+    residual = _activation(residual, "residual").contiguous()
+    if residual.dim() < 1 or residual.shape[-1] == 0:
+        raise ValueError("residual: expected [..., width]")
+    width = residual.shape[-1]
+    rows = residual.numel() // width
+    block = _like(block, residual, residual.shape, "block")
+    pre_weight = _like(pre_weight, residual, (width,), "pre_weight", torch.float32)
+    post_weight = _like(post_weight, residual, (width,), "post_weight", torch.float32)
+    if block is None and (gate is not None or post_weight is not None):
+        raise ValueError("gate and post_weight belong to a block")
+    per = 1
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() < 1 or gate.shape[-1] != width:
+            raise ValueError(f"gate: expected [..., {width}]")
+        gates = gate.numel() // width
+        per = rows // gates if rows_per_gate is None and gates else (rows_per_gate or 1)
+        if per < 1 and rows:
+            raise ValueError("rows_per_gate must be positive, and there are not more gates than rows")
+        per = max(per, 1)
+        if gates != -(-rows // per):
+            raise ValueError(f"{gates} gate rows of {per} rows each do not fit {rows} rows")
+        gate = _like(gate, residual, gate.shape, "gate")
+    desc = nat.bconv_block_norm_desc_t(rows, per, width, _DTYPES[residual.dtype], residual_scale, eps)
+    return residual, block, pre_weight, post_weight, gate, desc
+
+
+def block_norm(residual, block=None, *, pre_weight=None, post_weight=None, gate=None, rows_per_gate=None,
+               residual_scale=1.0, eps=1e-6) -> BlockNorm:
+    """The norm behind a block, its gate and residual scale, the residual sum and the next norm.
+
+    ``p = block * rsqrt(mean(block^2) + eps) * post_weight`` (``post_weight=None``: p = block),
+    ``residual_out = residual + residual_scale * gate * p`` and ``normed = residual_out *
+    rsqrt(mean(residual_out^2) + eps) * pre_weight`` (``pre_weight=None``: no ``normed``), over
+    rows of the last dimension.  residual, block and gate have one dtype, the weights are float32.
+    gate [..., width]: its row g holds for ``rows_per_gate`` consecutive rows (default: rows / gate
+    rows).  ``block=None`` (the norm before the first block) returns residual itself.
+    """
+    if block is None and pre_weight is None:
+        raise ValueError("without a block there is only the norm: give pre_weight")
+    given = residual
+    residual, block, pre_weight, post_weight, gate, desc = _block_norm_args(
+        residual, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps)
+    if not _is_current(residual):
+        with _on(residual):
+            return _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc)
+    return _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc)
+
+
+def _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc):
+    out = torch.empty_like(residual) if block is not None else None
+    normed = torch.empty_like(residual) if pre_weight is not None else None
+    nat.bconv_block_norm_forward(desc, _ptr(residual), _ptr(block), _ptr(gate), _ptr(post_weight), _ptr(pre_weight),
+                                 _ptr(out), _ptr(normed), _stream(residual))
+    return BlockNorm(given if out is None else out, normed)
+
+
+def block_norm_backward(residual_out, block=None, *, pre_weight=None, post_weight=None, gate=None,
+                        rows_per_gate=None, residual_scale=1.0, eps=1e-6, d_residual_out=None,
+                        d_normed=None) -> BlockNormGrad:
+    """The gradient of :func:`block_norm` at the residual it returned and the block it was given.
+
+    Takes the gradients of residual_out and normed (either may be None) and returns those of
+    residual, block, the weights and the gate (None where the forward had none); the sums
+    over rows are float32.
+    """
+    residual_out, block, pre_weight, post_weight, gate, desc = _block_norm_args(
+        residual_out, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps)
+    d_residual_out = _like(d_residual_out, residual_out, residual_out.shape, "d_residual_out")
+    d_normed = _like(d_normed, residual_out, residual_out.shape, "d_normed")
+    if d_normed is not None and pre_weight is None:
+        raise ValueError("d_normed needs pre_weight")
+    args = (residual_out, block, pre_weight, post_weight, gate, desc, d_residual_out, d_normed)
+    if not _is_current(residual_out):
+        with _on(residual_out):
+            return _block_norm_backward_run(*args)
+    return _block_norm_backward_run(*args)
+
+
+def _block_norm_backward_run(residual_out, block, pre_weight, post_weight, gate, desc, d_residual_out, d_normed):
+    def sums(t):
+        return None if t is None else torch.empty(t.shape, dtype=torch.float32, device=t.device)
+
+    g = BlockNormGrad(torch.empty_like(residual_out), None if block is None else torch.empty_like(block),
+                      sums(pre_weight), sums(post_weight), sums(gate))
+    need = nat.bconv_block_norm_workspace_bytes(desc)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=residual_out.device)
+    nat.bconv_block_norm_backward(desc, _ptr(residual_out), _ptr(block), _ptr(gate), _ptr(post_weight),
+                                  _ptr(pre_weight), _ptr(d_residual_out), _ptr(d_normed), _ptr(g.d_residual),
+                                  _ptr(g.d_block), _ptr(g.d_pre_weight), _ptr(g.d_post_weight), _ptr(g.d_gate),
+                                  _ptr(ws), _stream(residual_out))
+    return g
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: torch.Tensor | None
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: torch.Tensor | None
+    top_index: torch.Tensor | None
+
+
+def _logits(logits):
+    _activation(logits, "logits")
+    if logits.dim() < 1 or logits.shape[-1] == 0:
+        raise ValueError("logits: expected [..., vocab]")
+    return _rows(logits)
+
+
+def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0) -> TokenLogprobs:
+    """Log probabilities of given tokens, entropy, log-sum-exp and the top alternatives of logits / temperature.
+
+    logits [..., vocab]; tokens int64 [...] (a negative one: the row has no token, its logprob is 0;
+    one outside the vocabulary: NaN).  Returns float32 [...] (``top_logprob`` float32 and ``top_index``
+    int32 [..., top], in descending order of the logits, equal ones by ascending index).
+    """
+    lead = logits.shape[:-1]
+    x, rows, stride = _logits(logits)
+    tokens = _like(tokens, x, lead, "tokens", torch.int64)
+    desc = nat.bconv_token_desc_t(rows, stride, x.shape[-1], _DTYPES[x.dtype], top, temperature)
+    if not _is_current(x):
+        with _on(x):
+            return _token_logprobs_run(x, tokens, lead, top, desc)
+    return _token_logprobs_run(x, tokens, lead, top, desc)
+
+
+def _token_logprobs_run(x, tokens, lead, top, desc):
+    f32 = dict(dtype=torch.float32, device=x.device)
+    r = TokenLogprobs(torch.empty(lead, **f32) if tokens is not None else None, torch.empty(lead, **f32),
+                      torch.empty(lead, **f32), torch.empty(lead + (top,), **f32) if top > 0 else None,
+                      torch.empty(lead + (top,), dtype=torch.int32, device=x.device) if top > 0 else None)
+    nat.bconv_token_logprobs_forward(desc, _ptr(x), _ptr(tokens), _ptr(r.logprob), _ptr(r.entropy), _ptr(r.lse),
+                                     _ptr(r.top_logprob), _ptr(r.top_index), _stream(x))
+    return r
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, *, d_logprob=None, d_entropy=None, temperature=1.0):
+    """The gradient of the logits from those of logprob and entropy (either may be None).
+
+    lse and entropy are what :func:`token_logprobs` returned for these logits; the result has
+    the logits' dtype.  entropy may be None without d_entropy, tokens without d_logprob.
+    """
+    lead = logits.shape[:-1]
+    x, rows, stride = _logits(logits)
+    tokens = _like(tokens, x, lead, "tokens", torch.int64)
+    lse, entropy, d_logprob, d_entropy = (
+        _like(t, x, lead, name, torch.float32)
+        for t, name in ((lse, "lse"), (entropy, "entropy"), (d_logprob, "d_logprob"), (d_entropy, "d_entropy")))
+    if lse is None or (d_logprob is not None and tokens is None) or (d_entropy is not None and entropy is None):
+        raise ValueError("lse is needed, tokens with d_logprob, entropy with d_entropy")
+    desc = nat.bconv_token_desc_t(rows, stride, x.shape[-1], _DTYPES[x.dtype], 0, temperature)
+    with _on(x):
+        out = torch.empty(logits.shape, dtype=x.dtype, device=x.device)
+        nat.bconv_token_logprobs_backward(desc, _ptr(x), _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(d_logprob),
+                                          _ptr(d_entropy), _ptr(out), x.shape[-1], _stream(x))
+    return out

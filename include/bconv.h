@@ -346,6 +346,161 @@ bconv_status_t bfc_profile_stride(bfc_handle_t h, int32_t every);
 bconv_status_t bfc_destroy(bfc_handle_t h);
 
 /* ------------------------------------------------------------------------------------
+ * Operators of a language model around its low-bit layers.  A model whose large layers are
+ * binary keeps some at more bits (the first and last, the vocabulary), normalises and adds
+ * what a block returns, and reads its answer from the last layer's logits.  (The pages
+ * describe none of these; they stand beside the bfc_* layer and read what it writes.)
+ *
+ * Conventions beyond those at the top of this file:
+ *   - Activations are fp32, bf16 or fp16 (bconv_dtype_t), rows of consecutive elements; any
+ *     element-aligned address is accepted, 16-byte alignment (rows included) is fastest.
+ *   - Nothing here keeps state between calls: a workspace, where one is needed, belongs to
+ *     the caller and to one call at a time, and a quant-FC handle is read-only after its
+ *     creation, so calls on several streams may overlap.
+ *   - Calls run on the device that is current (bfc_quant_*: the device the handle was created
+ *     on), are asynchronous on `stream`, allocate nothing and can be captured into a graph.
+ *   - Every sum is held in fp32; results do not depend on timing (no atomics on floats).
+ *   - rows == 0 is no work (OK); the operands are not looked at.
+ * ------------------------------------------------------------------------------------ */
+
+/* Element types of activations. */
+typedef enum { BCONV_DTYPE_F32 = 0, BCONV_DTYPE_BF16 = 1, BCONV_DTYPE_F16 = 2 } bconv_dtype_t;
+
+/*
+ * Fully-connected layer with 4-bit weights and group scales:
+ *
+ *     out[r][c] = act( sum_f in[r][f] * W[c][f] + bias[c] ),
+ *     W[c][f] = scale[c][f / group_size] * (code[c][f] - zero[c][f / group_size])
+ *
+ * The codes (0..15) enter the sums as exact integers code - zero; each group's sum is scaled
+ * in fp32, so the weights themselves are never rounded.
+ *   in_channels, out_channels  1 .. 2^20.
+ *   group_size  32, 64, a multiple of 128, or >= in_channels (one group per output channel);
+ *               the last group of a row may be partial.
+ *   neuron      bconv_neuron_t;  in_dtype, out_dtype  bconv_dtype_t.
+ */
+typedef struct {
+  int32_t in_channels, out_channels, group_size;
+  int32_t neuron;
+  int32_t in_dtype, out_dtype;
+} bfc_quant_desc_t;
+
+typedef struct bfc_quant_handle_s* bfc_quant_handle_t;
+
+/*
+ * Create a layer on the current device; the weights are laid out for the kernels once.  The
+ * arrays may be host or device memory and are read during the call only (device arrays must
+ * be complete when the call is made; it does not wait for other streams).
+ *   codes  uint8 [out_channels][ceil(in_channels/2)], channel f in the low (f even) or high (f
+ *          odd) four bits of byte f / 2.
+ *   scale  float [out_channels][groups], groups = ceil(in_channels / group_size).
+ *   zero   uint8 [out_channels][groups], 0..15 (higher bits are ignored), or NULL (8).
+ *   bias   float [out_channels] or NULL (0).
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes, group_size), OOM, CUDA, NO_DEVICE.
+ */
+bconv_status_t bfc_quant_create(const bfc_quant_desc_t* desc, const uint8_t* codes, const float* scale,
+                                const uint8_t* zero, const float* bias, bfc_quant_handle_t* out);
+
+/* Bytes of workspace a forward over `rows` rows may need (0: none; -1: bad handle or rows). */
+int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, int64_t rows);
+
+/*
+ * in (device, row r at in + r * in_stride elements, in_channels each) -> out (device, row
+ * stride out_stride).  workspace: device, 256-byte aligned, bfc_quant_workspace_bytes(h, rows)
+ * bytes (NULL when that is 0), used until the work on `stream` completes.  Elements between a
+ * row's end and its stride are neither read nor written.  Errors: INVALID_ARG (also strides
+ * below the channel counts, rows < 0 or above 2^24, a missing or misaligned workspace), CUDA.
+ */
+bconv_status_t bfc_quant_forward(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows, void* out,
+                                 int64_t out_stride, void* workspace, struct CUstream_st* stream);
+int32_t bfc_quant_input_feature_channels(bfc_quant_handle_t h);
+int32_t bfc_quant_output_feature_channels(bfc_quant_handle_t h);
+bconv_status_t bfc_quant_sync_status(bfc_quant_handle_t h, struct CUstream_st* stream);
+bconv_status_t bfc_quant_destroy(bfc_quant_handle_t h);
+
+/*
+ * What stands between two blocks, over `rows` rows of `width` channels:
+ *
+ *     p = block * rsqrt(mean(block^2) + eps) * post_weight   (post_weight NULL: p = block)
+ *     residual_out = residual + residual_scale * gate * p    (gate NULL: 1)
+ *     normed = residual_out * rsqrt(mean(residual_out^2) + eps) * pre_weight
+ *
+ * the norm behind the block that returned `block`, its gate and residual scale, the residual
+ * sum, and the norm before the next block (of the unrounded sum).  Rows g * rows_per_gate ..
+ * (g + 1) * rows_per_gate - 1 share row g of `gate` ([ceil(rows / rows_per_gate)][width]).
+ * residual, block, gate, residual_out and normed are contiguous, of type dtype; the weights
+ * are fp32 [width].  block NULL: residual_out (which may be NULL) = residual, post_weight and
+ * gate must be NULL.  pre_weight and normed are both NULL or both given.  residual_out may be
+ * residual or block, and normed may be block; other overlaps are not allowed.
+ * width 1 .. 32768.  Errors: INVALID_ARG, UNSUPPORTED (width), CUDA, NO_DEVICE.
+ */
+typedef struct {
+  int64_t rows, rows_per_gate; /* rows_per_gate >= 1; read with a gate only */
+  int32_t width, dtype;
+  float residual_scale, eps;   /* eps >= 0 */
+} bconv_block_norm_desc_t;
+
+bconv_status_t bconv_block_norm_forward(const bconv_block_norm_desc_t* desc, const void* residual, const void* block,
+                                        const void* gate, const float* post_weight, const float* pre_weight,
+                                        void* residual_out, void* normed, struct CUstream_st* stream);
+
+/*
+ * The gradient of bconv_block_norm_forward at (residual_out, block): from d_residual_out and
+ * d_normed (either may be NULL: zero; d_normed needs pre_weight) to
+ *   d_residual, d_block  of type dtype (either may be NULL),
+ *   d_pre_weight, d_post_weight  fp32 [width], d_gate  fp32 [ceil(rows/rows_per_gate)][width]
+ *                        (each NULL or given with its operand); sums over rows in a fixed order.
+ * block NULL: as in the forward (d_block must be NULL).  d_residual may be d_residual_out or
+ * d_normed, and d_block may be the other one of them; other overlaps are not allowed.
+ * workspace: device, 256-byte aligned, of bconv_block_norm_workspace_bytes(desc) bytes; may be
+ * NULL when none of the three sums is asked for.  With rows == 0 the sums are set to 0.
+ */
+int64_t bconv_block_norm_workspace_bytes(const bconv_block_norm_desc_t* desc);
+bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* desc, const void* residual_out,
+                                         const void* block, const void* gate, const float* post_weight,
+                                         const float* pre_weight, const void* d_residual_out, const void* d_normed,
+                                         void* d_residual, void* d_block, float* d_pre_weight, float* d_post_weight,
+                                         float* d_gate, void* workspace, struct CUstream_st* stream);
+
+/*
+ * What rows of logits say.  With x = logits / temperature, per row:
+ *   lse      log sum_v exp x_v                                  fp32 [rows]
+ *   entropy  lse - sum_v p_v x_v, p = exp(x - lse)              fp32 [rows]
+ *   logprob  x[token] - lse                                     fp32 [rows], with tokens
+ *   top_logprob, top_index  the `top` largest logits in descending order, equal ones by
+ *            ascending index, as x - lse and the index          fp32 / int32 [rows][top]
+ * Row r of the logits starts at logits + r * stride elements; 1 <= vocab <= 2^30 entries.
+ * tokens: int64 [rows] or NULL (then logprob must be NULL); a negative token means that the
+ * row has none (logprob 0), one >= vocab gives NaN.  0 <= top <= min(64, vocab).  Masked
+ * entries of -infinity have probability 0; a row of nothing else has lse -infinity, entropy 0
+ * and logprob -infinity.  A NaN or +infinity makes its row's lse, entropy and log
+ * probabilities NaN; a NaN ranks above every number in top_index.
+ * Any output but top's pair may be NULL.
+ */
+typedef struct {
+  int64_t rows, stride;
+  int32_t vocab, dtype, top;
+  float temperature; /* finite, > 0 */
+} bconv_token_desc_t;
+
+bconv_status_t bconv_token_logprobs_forward(const bconv_token_desc_t* desc, const void* logits, const int64_t* tokens,
+                                            float* logprob, float* entropy, float* lse, float* top_logprob,
+                                            int32_t* top_index, struct CUstream_st* stream);
+
+/*
+ * The gradient of logprob and entropy (lse and entropy as the forward gave them):
+ *   d_logits[v] = ( d_logprob * ([v == token] - p_v) - d_entropy * p_v (x_v - lse + entropy) ) / temperature
+ * d_logprob (needs tokens) and d_entropy: fp32 [rows], either may be NULL (zero).  Rows without
+ * a token take no part in d_logprob; a token >= vocab makes its row NaN where d_logprob is given; a
+ * row of -infinity alone gets zeros.  d_logits: of type dtype, row stride d_stride; it may be
+ * the logits themselves (same stride).  desc->top is not read.
+ */
+bconv_status_t bconv_token_logprobs_backward(const bconv_token_desc_t* desc, const void* logits,
+                                             const int64_t* tokens, const float* lse, const float* entropy,
+                                             const float* d_logprob, const float* d_entropy, void* d_logits,
+                                             int64_t d_stride, struct CUstream_st* stream);
+
+/* ------------------------------------------------------------------------------------
  * Host helpers
  * ------------------------------------------------------------------------------------ */
 
