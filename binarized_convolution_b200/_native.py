@@ -121,7 +121,7 @@ _SIGS = {
     "bconv_staging": (_I32, [_P]),
     "bfc_tc_codes": (_I32, [_P]),
     "bfc_quant_create": (_I32, [ctypes.POINTER(bfc_quant_desc_t), _P, _P, _P, _P, ctypes.POINTER(_P)]),
-    "bfc_quant_workspace_bytes": (_I64, [_P, _I64]),
+    "bfc_quant_workspace_bytes": (_I64, [_P, _P, _I64, _I64]),
     "bfc_quant_forward": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P]),
     "bfc_quant_input_feature_channels": (_I32, [_P]),
     "bfc_quant_output_feature_channels": (_I32, [_P]),
@@ -442,8 +442,8 @@ def bfc_quant_create(desc: bfc_quant_desc_t, codes_ptr: int, scale_ptr: int, zer
     return h
 
 
-def bfc_quant_workspace_bytes(h, rows: int) -> int:
-    return load_library().bfc_quant_workspace_bytes(h, int(rows))
+def bfc_quant_workspace_bytes(h, in_ptr: int, in_stride: int, rows: int) -> int:
+    return load_library().bfc_quant_workspace_bytes(h, in_ptr, in_stride, rows)
 
 
 def bfc_quant_forward(h, in_ptr: int, in_stride: int, rows: int, out_ptr: int, out_stride: int,

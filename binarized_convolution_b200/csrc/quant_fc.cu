@@ -188,9 +188,10 @@ bconv_status_t bfc_quant_create(const bfc_quant_desc_t* d, const uint8_t* codes,
   return BCONV_OK;
 }
 
-int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, int64_t rows) {
-  if (!valid(h) || rows < 0 || rows > kMaxRows) return -1;
-  return 0;
+int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows) {
+  if (!valid(h) || rows < 0 || rows > kMaxRows || in_stride < h->desc.in_channels) return -1;
+  if (rows == 0 || quant_fc_tma_reads(in, in_stride, h->desc.in_channels, h->desc.in_dtype)) return 0;
+  return quant_fc_tc_workspace(rows, h->desc.in_channels, h->desc.in_dtype);
 }
 
 bconv_status_t bfc_quant_forward(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows, void* out,
@@ -200,13 +201,13 @@ bconv_status_t bfc_quant_forward(bfc_quant_handle_t h, const void* in, int64_t i
       !aligned_elem(out, h->desc.out_dtype) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return BCONV_ERR_INVALID_ARG;
   if (rows == 0) return BCONV_OK;
-  if (!in || !out) return BCONV_ERR_INVALID_ARG;
+  if (!in || !out || (!workspace && bfc_quant_workspace_bytes(h, in, in_stride, rows) > 0)) return BCONV_ERR_INVALID_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return BCONV_ERR_CUDA;
   QuantFcArgs a{h->codes,  h->scale, h->zero,           h->bias,              in,        out,        h->err,  in_stride,
                 out_stride, rows,    h->desc.in_channels, h->desc.out_channels, h->no_pad, h->k_tiles, h->group,
                 h->desc.neuron == BCONV_NEURON_RELU};
-  return from_cuda(launch_quant_fc_simt(a, h->desc.in_dtype, h->desc.out_dtype, stream));
+  return from_cuda(launch_quant_fc_tc(a, h->desc.in_dtype, h->desc.out_dtype, workspace, stream));
 }
 
 int32_t bfc_quant_input_feature_channels(bfc_quant_handle_t h) { return valid(h) ? h->desc.in_channels : -1; }

@@ -33,6 +33,10 @@ struct QuantFcArgs {
   int relu;
 };
 
-cudaError_t launch_quant_fc_simt(const QuantFcArgs& a, int in_dtype, int out_dtype, cudaStream_t s);
+// Whether the tensor-core kernel reads these rows as they are (else they are staged in the workspace,
+// of quant_fc_tc_workspace bytes).
+bool quant_fc_tma_reads(const void* in, int64_t in_stride, int k, int in_dtype);
+int64_t quant_fc_tc_workspace(int64_t rows, int k, int in_dtype);
+cudaError_t launch_quant_fc_tc(const QuantFcArgs& a, int in_dtype, int out_dtype, void* workspace, cudaStream_t s);
 
 }  // namespace bconv

@@ -162,7 +162,7 @@ class QuantFC(_Layer):
         to, _, out_stride = _rows(out)
         if to.data_ptr() != out.data_ptr():
             raise ValueError("out must have contiguous channels, and rows without gaps unless it is a matrix")
-        need = nat.bfc_quant_workspace_bytes(self.handle, rows)
+        need = nat.bfc_quant_workspace_bytes(self.handle, x.data_ptr(), in_stride, rows)
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need > 0 else None
         nat.bfc_quant_forward(self.handle, x.data_ptr(), in_stride, rows, to.data_ptr(), out_stride, _ptr(ws),
                               _stream(x))

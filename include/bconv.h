@@ -401,13 +401,15 @@ typedef struct bfc_quant_handle_s* bfc_quant_handle_t;
 bconv_status_t bfc_quant_create(const bfc_quant_desc_t* desc, const uint8_t* codes, const float* scale,
                                 const uint8_t* zero, const float* bias, bfc_quant_handle_t* out);
 
-/* Bytes of workspace a forward over `rows` rows may need (0: none; -1: bad handle or rows). */
-int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, int64_t rows);
+/* Bytes of workspace a forward of these rows needs (0: none; -1: bad handle, stride or rows): space to
+ * stage rows that the tensor cores' copies cannot read as they are (fp32, in not 16-byte aligned, in_stride not
+ * a multiple of 8, in_channels < 64). */
+int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows);
 
 /*
  * in (device, row r at in + r * in_stride elements, in_channels each) -> out (device, row
- * stride out_stride).  workspace: device, 256-byte aligned, bfc_quant_workspace_bytes(h, rows)
- * bytes (NULL when that is 0), used until the work on `stream` completes.  Elements between a
+ * stride out_stride).  workspace: device, 256-byte aligned, of bfc_quant_workspace_bytes(h, in,
+ * in_stride, rows) bytes (NULL when that is 0), used until the work on `stream` completes.  Elements between a
  * row's end and its stride are neither read nor written.  Errors: INVALID_ARG (also strides
  * below the channel counts, rows < 0 or above 2^24, a missing or misaligned workspace), CUDA.
  */

@@ -165,7 +165,7 @@ def test_quant_fc_no_rows_and_refusals():
                dict(out_ptr=None), dict(in_ptr=x.data_ptr() + 1), dict(workspace_ptr=x.data_ptr() + 16)):
         with pytest.raises(bc.BconvError):
             bc.bfc_quant_forward(h, **{**args, **kw})
-    assert bc.bfc_quant_workspace_bytes(h, -1) == -1
+    assert bc.bfc_quant_workspace_bytes(h, x.data_ptr(), 64, -1) == -1
     fc.close()
     with pytest.raises(ValueError):
         fc(x)

@@ -50,7 +50,7 @@ def test_quant_create_refuses_missing_arrays_and_handles():
     junk = ctypes.cast((ctypes.c_uint32 * 64)(), ctypes.c_void_p)
     for h in (None, junk):
         assert lib.bfc_quant_forward(h, P, 64, 1, P, 8, None, None) == INVALID
-        assert lib.bfc_quant_workspace_bytes(h, 1) == -1
+        assert lib.bfc_quant_workspace_bytes(h, P, 64, 1) == -1
         assert lib.bfc_quant_input_feature_channels(h) == -1
         assert lib.bfc_quant_output_feature_channels(h) == -1
         assert lib.bfc_quant_sync_status(h, None) == INVALID
