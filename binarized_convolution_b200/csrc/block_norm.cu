@@ -22,6 +22,7 @@
 #include "common.cuh"
 #include "dtype.cuh"
 #include "host_util.cuh"
+#include "tc_device.cuh"
 
 namespace bconv {
 namespace {
@@ -33,15 +34,16 @@ constexpr int kSumRows = 16;  // partial rows a column of the final sums is spli
 // accesses; C % 8 == 0 and every row 16-byte aligned), else one channel per access, a warp's side
 // by side.
 template <bool VEC>
-__device__ __forceinline__ int channel(int j, int e) {
-  const int t = static_cast<int>(blockDim.x), i = static_cast<int>(threadIdx.x);
+__device__ __forceinline__ int channel(int j, int e, int t) {
+  const int i = static_cast<int>(threadIdx.x);
   return VEC ? (j * t + i) * 8 + e : (j * 8 + e) * t + i;
 }
 
+// (t: the threads that share a row)
 template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int j, int C, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* row, int j, int C, float (&v)[8], int t = blockDim.x) {
   if (VEC) {
-    const int c = channel<true>(j, 0);
+    const int c = channel<true>(j, 0, t);
     if (c < C) {
       Raw8<T> w;
       w.load(row + c);
@@ -53,16 +55,16 @@ __device__ __forceinline__ void load8(const T* row, int j, int C, float (&v)[8])
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = channel<false>(j, e);
+      const int c = channel<false>(j, e, t);
       v[e] = c < C ? to_f32(row[c]) : 0.f;
     }
   }
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8], int t = blockDim.x) {
   if (VEC) {
-    const int c = channel<true>(j, 0);
+    const int c = channel<true>(j, 0, t);
     if (c < C) {
       Raw8<T> w;
       w.pack(v);
@@ -71,32 +73,46 @@ __device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8]
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = channel<false>(j, e);
+      const int c = channel<false>(j, e, t);
       if (c < C) row[c] = from_f32<T>(v[e]);
     }
   }
 }
 
-// Sums of N values over the CTA, the same in every thread and in a fixed order.  `buf` is one of
-// two areas of 32 * N floats used in turn, so one barrier per call is enough.
+// Sums of N values over the CTA's first t threads (which meet at barrier 1), the same in every thread and in
+// a fixed order.  `buf` is one of two areas of 32 * N floats used in turn, so one barrier per call is enough.
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
+__device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int t = blockDim.x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int warps = static_cast<int>(blockDim.x) >> 5;
+  const int warps = t >> 5;
   if (warps == 1) return;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) buf[i * 32 + (threadIdx.x >> 5)] = v[i];
-  __syncthreads();
+  tcdev::named_barrier(static_cast<uint32_t>(t));
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < warps; ++w)
+  for (int i = 0; i < N; ++i) v[i] = static_cast<int>(threadIdx.x & 31) < warps ? buf[i * 32 + (threadIdx.x & 31)] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += buf[i * 32 + w];
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
+
+// The gate row of a row that only moves on: a 64-bit division costs as much as the rest of a row's
+// arithmetic, and the gate row seldom changes.
+struct GateRow {
+  int64_t index = -1, end = 0;
+  __device__ __forceinline__ int64_t of(int64_t row, int64_t per) {
+    if (row >= end) {
+      index = row / per;
+      end = (index + 1) * per;
+    }
+    return index;
+  }
+};
 
 struct FwdArgs {
   const void *residual, *block, *gate;
@@ -112,6 +128,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_fwd_kernel(const FwdAr
   __shared__ float sums[2][32];
   const int C = a.C;
   const float inv = 1.f / static_cast<float>(C);
+  GateRow gate_row;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float r[NV][8];
 #pragma unroll
@@ -137,7 +154,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_fwd_kernel(const FwdAr
         }
       }
       if (a.gate) {
-        const T* gr = static_cast<const T*>(a.gate) + row / a.per_gate * C;
+        const T* gr = static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float g[8];
@@ -215,9 +232,11 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
     }
   }
   float* gate_to = nullptr;  // where the current gate row's sum goes
+  GateRow gate_row;
   for (int64_t row = first; row < last; ++row) {
-    const T* const g_row = a.gate ? static_cast<const T*>(a.gate) + row / a.per_gate * C : nullptr;
-    if (a.sum_gate && (row == first || row % a.per_gate == 0)) {
+    const bool new_gate = a.gate && row >= gate_row.end;
+    const T* const g_row = a.gate ? static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C : nullptr;
+    if (a.sum_gate && new_gate) {
       if (SUMS_IN_REGS && gate_to) {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
@@ -226,7 +245,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
           for (int e = 0; e < 8; ++e) agate[j][e] = 0.f;
         }
       }
-      const int64_t g = row / a.per_gate, begin = g * a.per_gate, end = min(begin + a.per_gate, a.rows);
+      const int64_t g = gate_row.index, begin = g * a.per_gate, end = min(begin + a.per_gate, a.rows);
       if (begin < first) gate_to = a.sum_gate + (cta * 2) * C;
       else if (end > last) gate_to = a.sum_gate + (cta * 2 + 1) * C;
       else gate_to = a.d_gate + g * C;
@@ -378,15 +397,400 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
   }
 }
 
+// ---- many rows of middling width: rows come through a ring in shared memory ----
+//
+// Loading a row into registers and then reducing it leaves the memory idle during the reductions
+// unless many CTAs take turns, and registers limit those.  Here one thread requests whole rows with bulk
+// copies, as far ahead as the ring has room, and the threads read them from shared memory, the
+// backward twice (once for the sums, once for the results), so that registers hold little but sums; the
+// weights wait in shared memory too.
+// Rows need no alignment: a copy takes the 16-byte pieces that hold the row, which then lies at
+// the same offset from a 16-byte boundary as in memory.
+
+constexpr int kRingLow = 1024, kRingHigh = 8192;  // widths served
+constexpr int kRingNv = 2;                       // 8-channel vectors of a thread
+constexpr int kRingBytes = 216 * 1024;           // of an SM
+constexpr int kMaxRing = 4;
+
+// (Copies that were issued always arrive; the limit of a second only keeps a wait from being endless.)
+__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity) {
+  if (tcdev::mbar_try(bar, parity)) return;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (tcdev::mbar_try(bar, parity)) return;
+    const uint64_t t = tcdev::globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > tcdev::kTimeoutNs) return;
+  }
+}
+
+// Bytes of a row in a stage: the 16-byte pieces that may hold it.
+__host__ __device__ constexpr int ring_row(int C, int elem) { return (C * elem + 15) / 16 * 16 + 16; }
+
+// Requests row `row` of `rows` of up to N arrays, C channels each, into the stage `to` (one thread; everyone
+// has passed a barrier since the stage was last read).  Row i lies at to + i * ring_row(), plus its offset
+// from a 16-byte boundary.  Pieces that reach into the rows before and after are read whole, but not beyond
+// the array: at its edges plain copies fill in.
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void ring_request(uint64_t* full, uint8_t* to, const T* const (&src)[N], int C, int64_t row,
+                                             int64_t rows) {
+  const uint32_t bytes = static_cast<uint32_t>(C) * sizeof(T);
+  const int pitch = ring_row(C, sizeof(T));
+  if (VEC) {
+    uint32_t arrays = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) arrays += src[i] != nullptr;
+    tcdev::mbar_expect_tx(full, arrays * bytes);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (src[i]) tcdev::bulk_load(to + i * pitch, src[i] + row * C, bytes, full);
+  } else {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (src[i]) {
+        const T* p = src[i] + row * C;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), e = a + bytes, base = a & ~uintptr_t{15};
+        uintptr_t lo = base, hi = (e + 15) & ~uintptr_t{15};
+        if (row == 0 && lo != a) lo += 16;
+        if (row + 1 == rows && hi != e) hi -= 16;
+        T* const at = reinterpret_cast<T*>(to + i * pitch + (a - base));
+        if (lo > a)
+          for (int c = 0; reinterpret_cast<uintptr_t>(p + c) < lo; ++c) at[c] = p[c];
+        if (hi < e)
+          for (int c = static_cast<int>(reinterpret_cast<const T*>(hi) - p); c < C; ++c) at[c] = p[c];
+        tcdev::bulk_load(to + i * pitch + (lo - base), reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), full);
+        sum += static_cast<uint32_t>(hi - lo);
+      }
+    tcdev::mbar_expect_tx(full, sum);  // (the arrival: behind the plain copies)
+  }
+}
+
+// Where array i's row lies in a stage.
+template <typename T, bool VEC>
+__device__ __forceinline__ const T* ring_at(const uint8_t* stage, int i, const T* src, int C, int64_t row) {
+  const int shift = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(src + row * C) & 15u);
+  return reinterpret_cast<const T*>(stage + i * ring_row(C, sizeof(T)) + shift);
+}
+
+__device__ __forceinline__ void ring_init(uint64_t* full, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) tcdev::mbar_init(&full[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+}
+
+// Weights of a thread's channels in shared memory, read and written by that thread alone (so without barriers):
+// vector j's eight as two float4, side by side over the threads.
+struct OwnWeights {
+  float4* at;
+  __device__ __forceinline__ void put(int j, const float (&w)[8]) {
+    at[(2 * j) * blockDim.x + threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+    at[(2 * j + 1) * blockDim.x + threadIdx.x] = make_float4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void get(int j, float (&w)[8]) const {
+    const float4 a = at[(2 * j) * blockDim.x + threadIdx.x], b = at[(2 * j + 1) * blockDim.x + threadIdx.x];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+};
+// Two sets of them lie in front of the ring.
+__host__ __device__ constexpr int own_weight_bytes(int threads) { return threads * kRingNv * 8 * 4; }
+
+// alpha * gate * post of this thread's channels (either may be NULL: 1)
+template <typename T, bool VEC>
+__device__ __forceinline__ void put_gate_post(OwnWeights W, float alpha, const T* gate, const float* post, int C) {
+#pragma unroll
+  for (int j = 0; j < kRingNv; ++j) {
+    float g[8], w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = w[e] = 1.f;
+    if (gate) load8<VEC>(gate, j, C, g);
+    if (post) load8<VEC>(post, j, C, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= alpha * g[e];
+    W.put(j, w);
+  }
+}
+
+template <typename T, bool VEC, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block_norm_fwd_ring_kernel(const FwdArgs a, int stages) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float sums[2][32];
+  __shared__ uint64_t full[kMaxRing];
+  constexpr int NV = kRingNv;
+  const int C = a.C, stage_bytes = 2 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
+  OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
+  uint8_t* const ring = smem + 2 * own;
+  const float inv = 1.f / static_cast<float>(C);
+  ring_init(full, stages);
+  const int64_t step = gridDim.x;
+  const T* const src[2] = {static_cast<const T*>(a.residual), static_cast<const T*>(a.block)};
+  if (threadIdx.x < 32 && tcdev::elect_one())
+    for (int i = 0; i < stages && blockIdx.x + i * step < a.rows; ++i)
+      ring_request<T, VEC>(&full[i], ring + i * stage_bytes, src, C, blockIdx.x + i * step, a.rows);
+  __syncwarp();
+  if (a.pre)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      load8<VEC>(a.pre, j, C, w);
+      pre.put(j, w);
+    }
+  if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
+  int s = 0;
+  uint32_t parity = 0;
+  GateRow gate_row;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
+    if (a.gate && row >= gate_row.end)
+      put_gate_post<T, VEC>(gate_post, a.alpha, static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C, a.post, C);
+    ring_wait(&full[s], parity);
+    uint8_t* const stage = ring + s * stage_bytes;
+    const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const b_row = ring_at<T, VEC>(stage, 1, src[1], C, row);
+    float r[NV][8], b[NV][8], q[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      load8<VEC>(r_row, j, C, r[j]);
+      if (a.block) {
+        load8<VEC>(b_row, j, C, b[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[0] = fmaf(b[j][e], b[j][e], q[0]);
+      }
+    }
+    if (a.post) block_sums(q, sums[0]);
+    else __syncthreads();
+    if (threadIdx.x < 32 && row + stages * step < a.rows && tcdev::elect_one())  // everyone has read this stage
+      ring_request<T, VEC>(&full[s], stage, src, C, row + stages * step, a.rows);
+    __syncwarp();
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+    if (a.block) {
+      const float bs = a.post ? rsqrtf(fmaf(q[0], inv, a.eps)) : 1.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[8];
+        gate_post.get(j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[j][e] = fmaf(b[j][e] * bs, w[e], r[j][e]);
+      }
+    }
+    if (a.residual_out)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) store8<VEC>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+    if (a.normed) {
+      float t[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[0] = fmaf(r[j][e], r[j][e], t[0]);
+      block_sums(t, sums[1]);
+      const float rs = rsqrtf(fmaf(t[0], inv, a.eps));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[8];
+        pre.get(j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[j][e] = r[j][e] * rs * w[e];
+        store8<VEC>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
+      }
+    }
+    if (a.post && !a.normed) __syncthreads();  // (otherwise there are two barriers a row, and the areas alternate)
+  }
+}
+
+// As block_norm_bwd_kernel.  While the gate stays the same, d_post_weight and d_gate are one sum
+//     S = sum_rows a dR b bs     d_gate = w_post S     d_post_weight = g S
+// times what does not change, so registers hold S, and d_post_weight's partial sums (in memory) are brought up
+// to date with the gate.  A row's stage is requested again in the next row, behind the barrier that shows that
+// everyone is done with it.
+template <typename T, bool VEC, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block_norm_bwd_ring_kernel(const BwdArgs a, int stages) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float sums[2][3 * 32];
+  __shared__ uint64_t full[kMaxRing];
+  constexpr int NV = kRingNv;
+  const int C = a.C, stage_bytes = 4 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
+  OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
+  uint8_t* const ring = smem + 2 * own;
+  const float inv = 1.f / static_cast<float>(C);
+  const int64_t first = blockIdx.x * a.rows_per_cta, last = min(first + a.rows_per_cta, a.rows), cta = blockIdx.x;
+  ring_init(full, stages);
+  const T* const src[4] = {a.d_normed ? static_cast<const T*>(a.residual_out) : nullptr,
+                           static_cast<const T*>(a.d_normed), static_cast<const T*>(a.d_out),
+                           static_cast<const T*>(a.block)};
+  if (threadIdx.x < 32 && tcdev::elect_one())
+    for (int i = 0; i < stages && first + i < last; ++i)
+      ring_request<T, VEC>(&full[i], ring + i * stage_bytes, src, C, first + i, a.rows);
+  __syncwarp();
+  if (a.pre)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      load8<VEC>(a.pre, j, C, w);
+      pre.put(j, w);
+    }
+  if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
+  float apre[NV][8], sum[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) apre[j][e] = sum[j][e] = 0.f;
+  // the sum of the rows of one gate row goes where it belongs
+  float* gate_to = nullptr;
+  GateRow gate_row;
+  const T* g_row = nullptr;
+  bool flushed = false;
+  auto flush = [&]() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      if (gate_to) {
+        if (a.post) load8<VEC>(a.post, j, C, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = a.post ? w[e] * sum[j][e] : sum[j][e];
+        store8<VEC>(gate_to, j, C, w);
+      }
+      if (a.sum_post) {
+        float t[8];
+        if (g_row) load8<VEC>(g_row, j, C, w);
+        if (flushed) load8<VEC>(a.sum_post + cta * C, j, C, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float add = g_row ? w[e] * sum[j][e] : sum[j][e];
+          t[e] = flushed ? t[e] + add : add;
+        }
+        store8<VEC>(a.sum_post + cta * C, j, C, t);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[j][e] = 0.f;
+    }
+    flushed = true;
+  };
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t row = first; row < last; ++row) {
+    if (a.gate && row >= gate_row.end) {
+      if (g_row) flush();
+      const int64_t g = gate_row.of(row, a.per_gate), begin = g * a.per_gate;
+      g_row = static_cast<const T*>(a.gate) + g * C;
+      put_gate_post<T, VEC>(gate_post, a.alpha, g_row, a.post, C);
+      if (a.sum_gate) {
+        if (begin < first) gate_to = a.sum_gate + (cta * 2) * C;
+        else if (min(gate_row.end, a.rows) > last) gate_to = a.sum_gate + (cta * 2 + 1) * C;
+        else gate_to = a.d_gate + g * C;
+      }
+    }
+    ring_wait(&full[s], parity);
+    uint8_t* const stage = ring + s * stage_bytes;
+    const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const dn_row = ring_at<T, VEC>(stage, 1, src[1], C, row),
+            *const do_row = ring_at<T, VEC>(stage, 2, src[2], C, row), *const b_row = ring_at<T, VEC>(stage, 3, src[3], C, row);
+    float t[3] = {0.f, 0.f, 0.f};  // r'^2, u r', b^2
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (a.d_normed) {
+        float r[8], dn[8], w[8];
+        load8<VEC>(r_row, j, C, r);
+        load8<VEC>(dn_row, j, C, dn);
+        pre.get(j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          t[0] = fmaf(r[e], r[e], t[0]);
+          t[1] = fmaf(dn[e] * w[e], r[e], t[1]);
+        }
+      }
+      if (a.post) {
+        float b[8];
+        load8<VEC>(b_row, j, C, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[2] = fmaf(b[e], b[e], t[2]);
+      }
+    }
+    block_sums(t, sums[0]);
+    const int64_t next = row - 1 + stages;
+    if (threadIdx.x < 32 && row > first && next < last && tcdev::elect_one()) {
+      const int sp = s == 0 ? stages - 1 : s - 1;
+      ring_request<T, VEC>(&full[sp], ring + sp * stage_bytes, src, C, next, a.rows);
+    }
+    __syncwarp();
+    const float rs = rsqrtf(fmaf(t[0], inv, a.eps)), m = t[1] * inv * rs * rs;
+    const float bs = a.post ? rsqrtf(fmaf(t[2], inv, a.eps)) : 1.f, abs_ = a.alpha * bs;
+    float c[1] = {0.f}, v[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float dr[8], w[8];
+      if (a.d_out) {
+        load8<VEC>(do_row, j, C, dr);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dr[e] = 0.f;
+      }
+      if (a.d_normed) {
+        float r[8], dn[8];
+        load8<VEC>(r_row, j, C, r);
+        load8<VEC>(dn_row, j, C, dn);
+        pre.get(j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dr[e] = fmaf(rs, fmaf(dn[e], w[e], -r[e] * m), dr[e]);
+          apre[j][e] = fmaf(dn[e], r[e] * rs, apre[j][e]);
+        }
+      }
+      if (a.d_residual) store8<VEC>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
+      if (a.block) {
+        float b[8];
+        load8<VEC>(b_row, j, C, b);
+        gate_post.get(j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum[j][e] = fmaf(dr[e], b[e] * abs_, sum[j][e]);
+          v[j][e] = dr[e] * w[e];
+          c[0] = fmaf(v[j][e], b[e], c[0]);
+        }
+      }
+    }
+    if (a.block) {
+      float mb = 0.f;
+      if (a.post) {
+        block_sums(c, sums[1]);
+        mb = c[0] * inv * bs * bs;
+      }
+      if (a.d_block)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          float b[8];
+          load8<VEC>(b_row, j, C, b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e] = bs * (v[j][e] - b[e] * mb);
+          store8<VEC>(static_cast<T*>(a.d_block) + row * C, j, C, b);
+        }
+    }
+    if (!a.block || !a.post) __syncthreads();  // with both reductions, their areas alternate
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+  flush();
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (a.sum_pre) store8<VEC>(a.sum_pre + cta * C, j, C, apre[j]);
+}
+
 struct SumArgs {
   const float *sum_pre, *sum_post, *sum_gate;
   float *d_pre, *d_post, *d_gate;
   int64_t rows, per_gate, rows_per_cta;
-  int C, ctas;
+  int C, ctas, by_gate;
 };
 
-// The partial rows of 32 channels, added in a fixed order.  blockIdx.y: 0 d_pre, 1 d_post, 1 + i the gate
-// row that CTA i found begun (and the first to do so).
+// The partial rows of 32 channels, added in a fixed order.  blockIdx.y: 0 d_pre, 1 d_post, above that the gate
+// rows that several CTAs share: by the gate row (2 + g), or, with more gate rows than CTAs, by the CTA i that
+// found it begun and is the first to do so (1 + i).
 __global__ void block_norm_sum_kernel(const SumArgs a) {
   __shared__ float part[kSumRows][33];
   const int c = blockIdx.x * 32 + threadIdx.x, y = blockIdx.y;
@@ -401,9 +805,15 @@ __global__ void block_norm_sum_kernel(const SumArgs a) {
     from = a.sum_post;
     to = a.d_post;
   } else if (a.d_gate) {
-    const int64_t i = y - 1, start = i * a.rows_per_cta, g = start / a.per_gate, begin = g * a.per_gate;
-    if (begin == start || begin / a.rows_per_cta + 1 != i) return;
-    const int64_t end = min(begin + a.per_gate, a.rows);
+    int64_t g = y - 2, i;
+    if (a.by_gate) {
+      i = g * a.per_gate / a.rows_per_cta + 1;
+    } else {
+      i = y - 1;
+      g = i * a.rows_per_cta / a.per_gate;
+    }
+    const int64_t begin = g * a.per_gate, end = min(begin + a.per_gate, a.rows), start = i * a.rows_per_cta;
+    if (begin >= start || begin / a.rows_per_cta + 1 != i || end <= start) return;
     step = 2 * static_cast<int64_t>(a.C);
     from = a.sum_gate + i * step;
     extra = a.sum_gate + (i - 1) * step + a.C;
@@ -436,8 +846,35 @@ Shape shape_for(int C, int max_nv) {
   return {std::min(1024, round_up((vecs + nv - 1) / nv, 32)), nv};
 }
 
+// A ring kernel's threads, stages of `stage` bytes and CTAs per SM, of at most `ctas` (what its registers allow),
+// and the bytes of shared memory of a CTA.
+struct Ring {
+  int threads, stages, ctas, bytes;
+};
+Ring ring_for(int C, int stage, int ctas) {
+  Ring r;
+  r.threads = round_up((C + 8 * kRingNv - 1) / (8 * kRingNv), 32);
+  const int own = 2 * own_weight_bytes(r.threads);
+  r.ctas = std::max(1, std::min(ctas, kRingBytes / (own + 2 * stage)));
+  r.stages = std::max(2, std::min(kMaxRing, (kRingBytes / r.ctas - own) / stage));
+  r.bytes = own + r.stages * stage;
+  return r;
+}
+Ring fwd_ring(int C, int elem) { return ring_for(C, 2 * ring_row(C, elem), C <= 4096 ? 3 * 256 / round_up((C + 15) / 16, 32) : 1); }
+Ring bwd_ring(int C, int elem) { return ring_for(C, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1); }
+
+// Whether the ring serves rows of this width with `arrays` arrays (two stages fit).
+bool ring_serves(int C, int elem, int arrays) {
+  return C > kRingLow && C <= kRingHigh && 2 * (own_weight_bytes(round_up((C + 15) / 16, 32)) + arrays * ring_row(C, elem)) <= kRingBytes;
+}
+
+// Below two rows an SM there is nothing to request ahead, and the plain kernels start sooner.
+bool many_rows(int64_t rows) { return rows > 2 * current_sm_count(); }
+
 int64_t bwd_ctas(const bconv_block_norm_desc_t* d, int64_t* rows_per_cta) {
-  const int64_t most = static_cast<int64_t>(current_sm_count()) * 2;
+  const int elem = dtype_bytes(d->dtype);
+  const int64_t most =
+      static_cast<int64_t>(current_sm_count()) * (ring_serves(d->width, elem, 4) ? bwd_ring(d->width, elem).ctas : 2);
   const int64_t per = std::max<int64_t>(1, ceil_div(d->rows, most));
   if (rows_per_cta) *rows_per_cta = per;
   return d->rows > 0 ? ceil_div(d->rows, per) : 0;
@@ -473,6 +910,29 @@ template <typename T, int NV, bool VEC, int MAX_THREADS>
 cudaError_t launch_bwd(const BwdArgs& a, int64_t ctas, int threads, cudaStream_t s) {
   block_norm_bwd_kernel<T, NV, VEC, NV <= 2, MAX_THREADS><<<static_cast<unsigned>(ctas), threads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+template <typename Kern, typename Args>
+cudaError_t launch_ring(Kern kern, const Args& a, int64_t ctas, const Ring& r, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, r.bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(ctas), r.threads, r.bytes, s>>>(a, r.stages);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_fwd_ring(const FwdArgs& a, cudaStream_t s) {
+  const Ring r = fwd_ring(a.C, sizeof(T));
+  const int64_t ctas = std::min(a.rows, static_cast<int64_t>(current_sm_count()) * r.ctas);
+  if (r.threads <= 256) return launch_ring(block_norm_fwd_ring_kernel<T, VEC, 256>, a, ctas, r, s);
+  return launch_ring(block_norm_fwd_ring_kernel<T, VEC, 512>, a, ctas, r, s);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_bwd_ring(const BwdArgs& a, int64_t ctas, cudaStream_t s) {
+  const Ring r = bwd_ring(a.C, sizeof(T));
+  if (r.threads <= 256) return launch_ring(block_norm_bwd_ring_kernel<T, VEC, 256>, a, ctas, r, s);
+  return launch_ring(block_norm_bwd_ring_kernel<T, VEC, 512>, a, ctas, r, s);
 }
 
 // Calls f.operator()<T, NV, VEC, MAX_THREADS> for a row shape; the bound on the threads keeps the
@@ -530,6 +990,11 @@ bconv_status_t bconv_block_norm_forward(const bconv_block_norm_desc_t* d, const 
             d->rows,  gate ? d->rows_per_gate : 1, d->width, d->residual_scale, d->eps};
   const bool vec = d->width % 8 == 0 &&
                    all_aligned16({residual, block, gate, post_weight, pre_weight, residual_out, normed});
+  if (many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 2))
+    return from_cuda(with_dtype(d->dtype, [&](auto t) {
+      using T = decltype(t);
+      return vec ? launch_fwd_ring<T, true>(a, stream) : launch_fwd_ring<T, false>(a, stream);
+    }));
   const Shape sh = shape_for(d->width, 4);
   return from_cuda(with_dtype(
       d->dtype, [&](auto t) { return with_shape<decltype(t)>(sh, vec, RunFwd{a, sh.threads, stream}); }));
@@ -581,15 +1046,20 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   const bool vec = d->width % 8 == 0 && all_aligned16({residual_out, block, gate, d_residual_out, d_normed, post_weight,
                                                        pre_weight, d_residual, d_block, d_gate, workspace});
   const Shape sh = shape_for(d->width, 4);
-  e = with_dtype(d->dtype,
-                 [&](auto t) { return with_shape<decltype(t)>(sh, vec, RunBwd{a, ctas, sh.threads, stream}); });
+  const bool ring = many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 4);
+  e = with_dtype(d->dtype, [&](auto t) {
+    using T = decltype(t);
+    if (ring) return vec ? launch_bwd_ring<T, true>(a, ctas, stream) : launch_bwd_ring<T, false>(a, ctas, stream);
+    return with_shape<T>(sh, vec, RunBwd{a, ctas, sh.threads, stream});
+  });
   if (e != cudaSuccess || !sums) return from_cuda(e);
   SumArgs f{};
   f.sum_pre = a.sum_pre; f.sum_post = a.sum_post; f.sum_gate = a.sum_gate;
   f.d_pre = a.sum_pre ? d_pre_weight : nullptr; f.d_post = d_post_weight; f.d_gate = d_gate;
   f.rows = a.rows; f.per_gate = a.per_gate; f.rows_per_cta = rows_per_cta; f.C = a.C; f.ctas = static_cast<int>(ctas);
-  // one grid row more for each CTA boundary that may cut a gate row (1 + i for CTA i)
-  const unsigned ys = d_gate ? static_cast<unsigned>(1 + std::max<int64_t>(1, ctas)) : 2u;
+  const int64_t gates = d_gate ? ceil_div(a.rows, a.per_gate) : 0;
+  f.by_gate = gates < ctas;
+  const unsigned ys = static_cast<unsigned>(2 + (f.by_gate ? gates : ctas - 1));
   block_norm_sum_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.C, 32)), ys), dim3(32, kSumRows), 0, stream>>>(f);
   return from_cuda(cudaGetLastError());
 }

@@ -119,17 +119,6 @@ __device__ __forceinline__ void st_32x32(uint32_t taddr, const uint32_t (&v)[32]
       : "memory");
 }
 
-// True in one lane of the (converged) warp.  The compiler knows that a region behind this has one
-// active thread and issues the MMA, commit and copy instructions of it, which take warp-uniform
-// operands, directly; behind `lane == 0` each of them became a loop over the active lanes of some 90 cycles.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0, lane_id = 0;
-  asm volatile(
-      "{\n .reg .b32 r;\n .reg .pred p;\n elect.sync r|p, 0xffffffff;\n @p mov.s32 %0, 1;\n mov.s32 %1, r;\n}\n"
-      : "+r"(pred), "+r"(lane_id));
-  return pred != 0;
-}
-
 // 16 columns of this warp's 32 TMEM lanes; the values may be used after ld_wait of the same registers.
 __device__ __forceinline__ void ld_16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(

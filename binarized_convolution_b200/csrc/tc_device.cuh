@@ -21,6 +21,17 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// True in one lane of the (converged) warp.  The compiler knows that a region behind this has one
+// active thread and issues the MMA, commit and copy instructions of it, which take warp-uniform
+// operands, directly; behind `lane == 0` each of them became a loop over the active lanes of some 90 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0, lane_id = 0;
+  asm volatile(
+      "{\n .reg .b32 r;\n .reg .pred p;\n elect.sync r|p, 0xffffffff;\n @p mov.s32 %0, 1;\n mov.s32 %1, r;\n}\n"
+      : "+r"(pred), "+r"(lane_id));
+  return pred != 0;
+}
+
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
 }

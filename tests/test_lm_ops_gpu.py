@@ -244,6 +244,8 @@ NORM_SHAPES = [  # rows, width, rows per gate (0: no gate)
     (1, 1, 1), (1, 8, 0), (1, 4096, 1), (2, 7, 1), (3, 64, 2), (5, 100, 0), (17, 256, 5), (64, 1001, 64),
     (33, 2048, 1), (300, 512, 7), (700, 264, 1000), (150, 2056, 40), (40, 4096, 0), (900, 1024, 450), (9, 8192, 4),
     (6, 8200, 3), (4, 12345, 2), (7, 16384, 3), (3, 32768, 2), (2, 32761, 1),
+    (1200, 1032, 7), (700, 1500, 350), (900, 2047, 0), (640, 4096, 100), (500, 4099, 500), (400, 8192, 3), (310, 7001, 0),
+    (299, 1025, 1),
 ]
 
 
