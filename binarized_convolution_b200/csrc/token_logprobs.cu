@@ -4,18 +4,18 @@
 //
 // With x = logits / temperature and m the largest logit seen, each thread keeps
 //     s = sum exp((l - m) / temperature)     t = sum exp((l - m) / temperature) (l - m) / temperature
-// over its elements (rescaled when m grows), and these join pairwise, so a row is read once:
+// over its elements (in powers of 2; rescaled when m grows), and these join pairwise, so a row is read once:
 //     lse = m / temperature + log s          entropy = log s - t / s
-// Differences to m are taken before the scale, so logits of the type's lowest value (masks) stay
-// finite, and log probabilities are (l - m) / temperature - log s, exact where l is near m.
+// An element costs one fused multiply-add for the exponent, one exp2, one addition and one more
+// multiply-add (see Stat).
 //
 // Top alternatives: the k-th largest of the maxima of disjoint groups of elements is a lower
-// bound of the k-th largest element.  After a CTA's first elements it takes that bound from its
-// threads' maxima and from then on only collects elements that reach it (few, unless the row is
-// sorted); the collected ones are ordered by counting for each how many come before it.  If more
-// are found than the buffer holds (long runs of equal logits, sorted rows), a second pass uses the bound
-// of the whole row, and if that does not suffice either, k passes over the row pick one each.
-// Every path gives the same answer: logits in descending order, equal ones by index.
+// bound of the k-th largest element.  After its first 32 elements a thread, a CTA takes that bound from its
+// threads' maxima, and then only collects elements that reach it (few, unless the row is sorted); the
+// collected ones are ordered by counting for each how many come before it.  If more are found than the
+// buffer holds (long runs of equal logits, sorted rows), a second pass uses the bound of the whole row,
+// and if that does not suffice either, k passes over the row pick one each.  Every path gives the
+// same answer: logits in descending order, equal ones by index.
 //
 // A row is one CTA's work, or a cluster's where there are few rows; the cluster's CTAs hand their (m, s,
 // t) and their own top k to the first one through its shared memory.
@@ -38,7 +38,7 @@ constexpr int kMaxTop = 64;
 constexpr int kCap = 1024;       // collected elements of one CTA
 constexpr int kGroups = 128;     // groups of 4 threads whose maxima bound the k-th largest
 constexpr int kMaxCluster = 8;
-constexpr float kFar = -1e4f;    // exp of it and of anything below is 0; keeps 0 * d finite
+constexpr float kFar = -1e4f;    // exp2 of it and of anything below is 0; keeps 0 * d finite
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // 2^x by the hardware's approximation (relative error below 2^-22; -inf gives 0)
@@ -66,25 +66,98 @@ __device__ __forceinline__ unsigned long long entry(uint32_t key, uint32_t index
 }
 __device__ __forceinline__ uint32_t entry_index(unsigned long long e) { return 0xffffffffu - static_cast<uint32_t>(e); }
 
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// s and t relative to the largest logit m, in powers of 2 of units c = log2(e) / temperature: an element v counts
+// 2^d with d = v c - m c.  Usually ("near") m c is rounded once and v c - round(m c) is one exact
+// multiply-add; that shifts all d by the same rounding, of at most 2^-5 for |m c| < 2^20, which drops out
+// of every result as long as all use the same rounded product.  Beyond that the difference is taken first.
 struct Stat {
-  float m, s, t;  // s and t relative to the largest logit m, in units of 1 / temperature
+  float m, s, t;
 };
 
-// The same relative to a larger m (scale = 1 / temperature).
-__device__ __forceinline__ void raise(Stat& a, float m, float scale) {
+__device__ __forceinline__ bool near(float m, float c) { return fabsf(m * c) < 1048576.f && m > -1e30f; }
+
+// d of an element v
+__device__ __forceinline__ float relative(float v, float m, float c) {
+  return near(m, c) ? fmaf(v, c, -__fmul_rn(m, c)) : (v - m) * c;
+}
+
+// The same relative to a larger m.
+__device__ __forceinline__ void raise(Stat& a, float m, float c) {
   if (m > a.m) {
-    // with nothing but -inf so far s and t are 0 (or NaN, which stays)
-    const float d = a.m == -INFINITY ? -FLT_MAX : (a.m - m) * scale;
-    const float f = exp2_approx(d * kLog2e);
+    float d = -FLT_MAX;  // with nothing but -inf so far s and t are 0 (or NaN, which stays)
+    if (a.m != -INFINITY) {
+      if (near(a.m, c)) d = near(m, c) ? __fsub_rn(__fmul_rn(a.m, c), __fmul_rn(m, c)) : fmaf(-m, c, __fmul_rn(a.m, c));
+      else d = relative(a.m, m, c);
+    }
+    const float f = exp2_approx(d);
     a.t = fmaf(a.s, fmaxf(d, kFar), a.t) * f;
     a.s *= f;
     a.m = m;
   }
 }
-__device__ __forceinline__ Stat join(Stat a, Stat b, float scale) {
-  raise(a, b.m, scale);
-  raise(b, a.m, scale);
+__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
+  raise(a, b.m, c);
+  raise(b, a.m, c);
   return {a.m, a.s + b.s, a.t + b.t};
+}
+__device__ __forceinline__ Stat join_lanes(Stat st, float c) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat b;
+    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+    st = join(st, b, c);
+  }
+  return st;
+}
+
+// Adds one or eight elements whose largest is mx (NaN if one is).
+template <int N>
+__device__ __forceinline__ void add(Stat& st, const float (&v)[N], float mx, float c) {
+  raise(st, mx, c);
+  const float mc = __fmul_rn(st.m, c);
+  float s1 = 0.f, t1 = 0.f;
+  if (near(st.m, c)) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      // (-inf: p = exp2(kFar) = 0, with a finite product)
+      const float d = max_nan(fmaf(v[e], c, -mc), kFar), p = exp2_approx(d);
+      if (e & 1) {
+        s1 += p;
+        t1 = fmaf(p, d, t1);
+      } else {
+        st.s += p;
+        st.t = fmaf(p, d, st.t);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (v[e] != -INFINITY) {
+        const float d = max_nan((v[e] - st.m) * c, kFar), p = exp2_approx(d);
+        st.s += p;
+        st.t = fmaf(p, d, st.t);
+      }
+    }
+  }
+  st.s += s1;
+  st.t += t1;
+}
+
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) m = max_nan(m, v[e]);
+  return m;
 }
 
 struct FwdArgs {
@@ -95,6 +168,7 @@ struct FwdArgs {
   int64_t rows, stride;
   int vocab, top;
   float scale;  // 1 / temperature
+  float c;      // log2(e) / temperature
 };
 
 struct Shared {
@@ -103,7 +177,7 @@ struct Shared {
   unsigned long long top[kMaxCluster * kMaxTop];            // first CTA: every CTA's top entries
   unsigned long long best[kThreads / 32];                   // one round of the slow selection
   unsigned long long found[kCap];
-  uint32_t group[kGroups];
+  __align__(16) uint32_t group[kGroups];
   uint32_t bound;
   int count;
 };
@@ -140,9 +214,12 @@ __device__ __forceinline__ uint32_t bound_of(Shared& S, uint32_t mx, int top) {
   if (threadIdx.x < kGroups) {
     const uint32_t own = S.group[threadIdx.x];
     int before = 0;
-    for (int i = 0; i < kGroups; ++i) {
-      const uint32_t o = S.group[i];
-      before += o > own || (o == own && i < static_cast<int>(threadIdx.x));
+    const int at = threadIdx.x;
+#pragma unroll 8
+    for (int i = 0; i < kGroups; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&S.group[i]);
+      before += (o.x > own || (o.x == own && i < at)) + (o.y > own || (o.y == own && i + 1 < at)) +
+                (o.z > own || (o.z == own && i + 2 < at)) + (o.w > own || (o.w == own && i + 3 < at));
     }
     if (before == top - 1) S.bound = own;  // exactly one thread
   }
@@ -166,7 +243,7 @@ __device__ __forceinline__ void order_entries(const unsigned long long* from, in
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const FwdArgs a) {
   __shared__ Shared S;
   uint32_t rank, peers;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -178,72 +255,69 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdA
   const int begin = static_cast<int>(min(static_cast<int64_t>(rank) * part, static_cast<int64_t>(a.vocab)));
   const int end = static_cast<int>(min(static_cast<int64_t>(begin) + part, static_cast<int64_t>(a.vocab)));
   const int top = min(a.top, end - begin);  // this part's share of the candidates
-  const float scale = a.scale;
+  const float scale = a.scale, c2 = a.c;
   if (threadIdx.x == 0) S.count = 0;
   // (awaited before the first access to another CTA's shared memory: that CTA has started by then)
   if (peers > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  // first elements, for the bound on the top entries
-  uint32_t bound = 0;
-  if (top > 0) {
-    uint32_t mx = 0;
-    const int first = min(end, begin + kThreads * 8 + 16);
-    each(row, begin, first,
-         [&](int, const float (&v)[8]) {
-#pragma unroll
-           for (int e = 0; e < 8; ++e) mx = max(mx, order_key(v[e]));
-         },
-         [&](int, float v) { mx = max(mx, order_key(v)); });
-    bound = bound_of(S, mx, top);
-  }
-  __syncthreads();
-
+  // the part as [head][body: 16-byte aligned, 8 elements a step][tail]; every thread has one element of head
+  // and tail at most
   Stat st = {-INFINITY, 0.f, 0.f};
   const bool want = top > 0;
-  const float bound_value = bound ? key_value(bound) : -INFINITY;  // (NaN: only NaNs reach it)
-  auto add = [&](float v) {
-    const float d = v == -INFINITY ? -FLT_MAX : (v - st.m) * scale;  // (v <= m here, or NaN)
-    const float e = exp2_approx(d * kLog2e);
-    st.s += e;
-    st.t = fmaf(e, fmaxf(d, kFar), st.t);
+  const int head = min(end - begin, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(row + begin) & 15u)) & 15u) / sizeof(T)));
+  const int steps = (end - begin - head) / 8, ends = end - begin - steps * 8;
+  const T* const body = row + begin + head;
+  const bool has_end = static_cast<int>(threadIdx.x) < ends;
+  const int end_at = begin + static_cast<int>(threadIdx.x) + (static_cast<int>(threadIdx.x) < head ? 0 : steps * 8);
+  float edge[1] = {-INFINITY};
+  if (has_end) edge[0] = to_f32(row[end_at]);
+
+  constexpr int kBatch = 4;  // steps whose loads are in flight together
+  Raw8<T> w[kBatch];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (at + i * kThreads < steps) w[i].load(body + static_cast<int64_t>(at + i * kThreads) * 8);
   };
-  each(row, begin, end,
-       [&](int c, const float (&v)[8]) {
-         float mx = v[0];
-         bool nan = v[0] != v[0];
+  load(threadIdx.x);
+  uint32_t bound = 0;
+  float bound_value = -INFINITY;  // (NaN: only NaNs reach it)
+  if (want) {                     // the bound on the top entries from the first batch
+    uint32_t mx = has_end ? order_key(edge[0]) : 0u;
 #pragma unroll
-         for (int e = 1; e < 8; ++e) {
-           mx = fmaxf(mx, v[e]);
-           nan |= v[e] != v[e];
-         }
-         raise(st, mx, scale);
+    for (int i = 0; i < kBatch; ++i)
+      if (static_cast<int>(threadIdx.x) + i * kThreads < steps) {
+        float v[8];
+        w[i].unpack(v);
+        mx = max(mx, order_key(largest(v)));
+      }
+    bound = bound_of(S, mx, top);
+    if (bound) bound_value = key_value(bound);
+  }
+  if (has_end) {
+    add(st, edge, edge[0], c2);
+    if (want && order_key(edge[0]) >= bound) collect(S, order_key(edge[0]), end_at);
+  }
+  for (int at = threadIdx.x; at < steps; at += kBatch * kThreads) {
+    if (at != static_cast<int>(threadIdx.x)) load(at);
 #pragma unroll
-         for (int e = 0; e < 8; ++e) add(v[e]);
-         if (want && (!(mx < bound_value) || nan))
+    for (int i = 0; i < kBatch; ++i)
+      if (at + i * kThreads < steps) {
+        float v[8];
+        w[i].unpack(v);
+        const float mx = largest(v);
+        add(st, v, mx, c2);
+        if (want && !(mx < bound_value))
 #pragma unroll
-           for (int e = 0; e < 8; ++e) {
-             const uint32_t k = order_key(v[e]);
-             if (k >= bound) collect(S, k, c + e);
-           }
-       },
-       [&](int c, float v) {
-         raise(st, v, scale);
-         add(v);
-         if (want) {
-           const uint32_t k = order_key(v);
-           if (k >= bound) collect(S, k, c);
-         }
-       });
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t k = order_key(v[e]);
+            if (k >= bound) collect(S, k, begin + head + (at + i * kThreads) * 8 + e);
+          }
+      }
+  }
 
   // statistics of the CTA
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-    st = join(st, b, scale);
-  }
+  st = join_lanes(st, c2);
   if ((threadIdx.x & 31) == 0) S.stat[threadIdx.x >> 5] = st;
   __syncthreads();
 
@@ -306,9 +380,9 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdA
       }
     }
   }
-  if (threadIdx.x == 0) {
-    st = S.stat[0];
-    for (int w = 1; w < kThreads / 32; ++w) st = join(st, S.stat[w], scale);
+  if (threadIdx.x < 32) {
+    st = threadIdx.x < kThreads / 32 ? S.stat[threadIdx.x] : Stat{-INFINITY, 0.f, 0.f};
+    st = join_lanes(st, c2);
   }
   __syncthreads();
   int n = top;
@@ -331,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdA
     tcdev::cluster_sync();
     if (rank != 0) return;
     if (threadIdx.x == 0)
-      for (uint32_t p = 1; p < peers; ++p) st = join(st, S.peers[p], scale);
+      for (uint32_t p = 1; p < peers; ++p) st = join(st, S.peers[p], c2);
     if (a.top > 0) {
       // entries of 0 ("nothing") come last: there are at least a.top real ones
       for (int i = threadIdx.x; i < static_cast<int>(peers) * a.top; i += kThreads) S.found[i] = i < a.top && i >= top ? 0ull : S.top[i];
@@ -345,14 +419,16 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_fwd_kernel(const FwdA
   __syncthreads();
   st = S.stat[0];
   const bool nothing = st.m == -INFINITY && st.s == 0.f;
-  const float log_s = __log2f(st.s) * kLn2;
+  const float log2_s = __log2f(st.s);
   auto logprob = [&](float v) {
-    if (nothing || v == -INFINITY) return st.s != st.s ? st.s : -INFINITY;
-    return (v - st.m) * scale - log_s;
+    if (st.s != st.s) return st.s;
+    if (nothing || v == -INFINITY) return -INFINITY;
+    const float d = relative(v, st.m, c2);
+    return d < -1e30f ? (v - st.m) * scale : (d - log2_s) * kLn2;  // (far below: the product may have overflowed)
   };
   if (threadIdx.x == 0) {
-    if (a.lse) a.lse[r] = nothing ? -INFINITY : fmaf(st.m, scale, log_s);
-    if (a.entropy) a.entropy[r] = nothing ? 0.f : log_s - st.t / st.s;
+    if (a.lse) a.lse[r] = nothing ? -INFINITY : near(st.m, c2) ? (__fmul_rn(st.m, c2) + log2_s) * kLn2 : fmaf(st.m, scale, log2_s * kLn2);
+    if (a.entropy) a.entropy[r] = nothing ? 0.f : (log2_s - st.t / st.s) * kLn2;
     if (a.logprob) {
       const int64_t token = a.tokens[r];
       a.logprob[r] = token < 0 ? 0.f : token >= a.vocab ? __uint_as_float(0x7fc00000u) : logprob(to_f32(row[token]));
@@ -375,8 +451,8 @@ struct BwdArgs {
   float scale;
 };
 
-constexpr int kBwdThreads = 256;
-constexpr int kBwdStep = kBwdThreads * 8 * 4;  // elements of one CTA
+constexpr int kBwdThreads = 256, kBwdBatch = 4;
+constexpr int kBwdStep = kBwdThreads * 8 * kBwdBatch;  // elements of one CTA
 
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const BwdArgs a) {
@@ -385,46 +461,60 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const B
   const int end = min(a.vocab, begin + kBwdStep);
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   T* to = static_cast<T*>(a.d_logits) + r * a.d_stride;
-  const float lse = a.lse[r], h = a.d_entropy ? a.entropy[r] : 0.f;
-  const int64_t token = a.d_logprob ? a.tokens[r] : -1;
-  float g = 0.f;
-  if (token >= 0) g = token < a.vocab ? a.d_logprob[r] : __uint_as_float(0x7fc00000u);
-  const float ge = a.d_entropy ? a.d_entropy[r] : 0.f;
-  const float scale = a.scale;
-  auto grad = [&](int c, float v) {
-    // -inf: probability 0 (in a row of nothing else too)
-    const float logp = v == -INFINITY ? -INFINITY : fmaf(v, scale, -lse);
-    const float p = exp2_approx(logp * kLog2e);
-    float d = -p * (g + (p == 0.f ? 0.f : ge * (logp + h)));
-    if (c == token) d += g;
-    return d * scale;
-  };
   const bool vec = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(to)) & 15u) == 0;
-  if (vec) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + begin);
-    const int head = min(end - begin, static_cast<int>(((16 - (at & 15u)) & 15u) / sizeof(T)));
-    const int body = (end - begin - head) / 8, tail = begin + head + body * 8;
-    if (static_cast<int>(threadIdx.x) < head) {
-      const int c = begin + threadIdx.x;
-      to[c] = from_f32<T>(grad(c, to_f32(row[c])));
-    }
-    for (int i = threadIdx.x; i < body; i += kBwdThreads) {
-      const int c = begin + head + i * 8;
-      Raw8<T> w;
-      w.load(row + c);
-      float v[8];
-      w.unpack(v);
+  const int head = vec ? min(end - begin, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(row + begin) & 15u)) & 15u) / sizeof(T)))
+                       : 0;
+  const int steps = vec ? (end - begin - head) / 8 : 0, first = begin + head;
+  Raw8<T> w[kBwdBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = grad(c + e, v[e]);
-      w.pack(v);
-      w.store(to + c);
+  for (int i = 0; i < kBwdBatch; ++i) {
+    const int at = static_cast<int>(threadIdx.x) + i * kBwdThreads;
+    if (at < steps) w[i].load(row + first + at * 8);
+  }
+  const float scale = a.scale;
+  const int64_t token = a.d_logprob ? a.tokens[r] : -1;
+  float g = 0.f, ge = 0.f, h = 0.f, lse = a.lse[r];
+  if (token >= 0) g = token < a.vocab ? a.d_logprob[r] : __uint_as_float(0x7fc00000u);
+  if (a.d_entropy) {
+    ge = a.d_entropy[r];
+    h = a.entropy[r];
+  }
+  // d = p (k0 + k1 log p), and g / temperature more at the token
+  float k0 = -(g + ge * h) * scale, k1 = -ge * scale;
+  if (lse == -INFINITY) {  // nothing but -inf in the row: no gradient (a NaN of g stays)
+    lse = 0.f;
+    k0 *= 0.f;
+    k1 = 0.f;
+  }
+  auto grad = [&](float v) {
+    // (-inf: p = exp(kFar) = 0, with a finite product)
+    const float logp = max_nan(fmaf(v, scale, -lse), kFar);
+    return exp2_approx(logp * kLog2e) * fmaf(k1, logp, k0);
+  };
+  const float extra = g * scale;
+#pragma unroll
+  for (int i = 0; i < kBwdBatch; ++i) {
+    const int at = static_cast<int>(threadIdx.x) + i * kBwdThreads;
+    if (at < steps) {
+      const int c = first + at * 8;
+      float v[8];
+      w[i].unpack(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = grad(v[e]);
+      if (token >= c && token < c + 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e == token) v[e] += extra;
+      w[i].pack(v);
+      w[i].store(to + c);
     }
-    if (tail + static_cast<int>(threadIdx.x) < end) {
-      const int c = tail + threadIdx.x;
-      to[c] = from_f32<T>(grad(c, to_f32(row[c])));
-    }
-  } else {
-    for (int c = begin + threadIdx.x; c < end; c += kBwdThreads) to[c] = from_f32<T>(grad(c, to_f32(row[c])));
+  }
+  // the ragged ends (all of it where the rows' alignments differ)
+  for (int i = threadIdx.x; i < end - begin - steps * 8; i += kBwdThreads) {
+    const int c = i < head ? begin + i : begin + steps * 8 + i;
+    float d = grad(to_f32(row[c]));
+    if (c == token) d += extra;
+    to[c] = from_f32<T>(d);
   }
 }
 
@@ -437,10 +527,18 @@ bconv_status_t check_desc(const bconv_token_desc_t* d) {
 
 template <typename T>
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
-  // few rows: a cluster per row, as long as every CTA keeps a few thousand elements
-  const int sms = current_sm_count();
+  // CTAs per row: those that finish first, at two CTAs an SM, a CTA's fixed cost (the bound, the joins) being
+  // that of some 12000 elements (3 us)
+  const int64_t slots = 2 * static_cast<int64_t>(current_sm_count());
   unsigned peers = 1;
-  while (peers < kMaxCluster && a.rows * peers * 2 <= 2 * sms && a.vocab / static_cast<int>(peers) >= 4 * kThreads) peers *= 2;
+  double best = 1e300;
+  for (unsigned p = 1; p <= kMaxCluster; p *= 2) {
+    const double cost = static_cast<double>(ceil_div(a.rows * p, slots)) * (static_cast<double>(a.vocab) / p + 12000.0);
+    if (cost < best * 0.98) {
+      best = cost;
+      peers = p;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * peers);
   cfg.blockDim = dim3(kThreads);
@@ -474,7 +572,7 @@ bconv_status_t bconv_token_logprobs_forward(const bconv_token_desc_t* d, const v
   if (!logits || (d->top > 0) != (top_logprob != nullptr) || (d->top > 0) != (top_index != nullptr))
     return BCONV_ERR_INVALID_ARG;
   FwdArgs a{logits, tokens, logprob, entropy, lse, top_logprob, top_index, d->rows, d->stride, d->vocab, d->top,
-            1.f / d->temperature};
+            1.f / d->temperature, kLog2e / d->temperature};
   return from_cuda(with_dtype(d->dtype, [&](auto t) { return launch_fwd<decltype(t)>(a, stream); }));
 }
 
