@@ -10,11 +10,14 @@
 // multiply-add (see Stat).
 //
 // Top alternatives: the k-th largest of the maxima of disjoint groups of elements is a lower
-// bound of the k-th largest element.  After its first 32 elements a thread, a CTA takes that bound from its
-// threads' maxima, and then only collects elements that reach it (few, unless the row is sorted); the
-// collected ones are ordered by counting for each how many come before it.  If more are found than the
-// buffer holds (long runs of equal logits, sorted rows), a second pass uses the bound of the whole row,
-// and if that does not suffice either, k passes over the row pick one each.  Every path gives the
+// bound of the k-th largest element.  After its first batch of loads (32 elements a thread; fp32: 16), a CTA
+// takes that bound from its threads' maxima, and from then on a thread only notes the batches whose largest
+// element reaches it (few, unless the row is sorted).  At the end the threads' maxima of the whole part
+// give a closer bound; what reaches it is collected from the noted batches and ordered by counting for each
+// element how many come before it.  (Collecting elements while reading cost more than the reading: almost
+// every batch of a warp holds one that reaches the first bound.)  Where the notes or the collected
+// elements run over (sorted rows, long runs of equal logits), the part is read again with the closer bound,
+// and if that does not suffice either, k passes over it pick one each.  Every path gives the
 // same answer: logits in descending order, equal ones by index.
 //
 // A row is one CTA's work, or a cluster's where there are few rows; the cluster's CTAs hand their (m, s,
@@ -24,6 +27,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dtype.cuh"
@@ -33,10 +37,11 @@
 namespace bconv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtas = 4;          // CTAs an SM: enough that one's joins hide behind another's loads
 constexpr int kMaxTop = 64;
-constexpr int kCap = 1024;       // collected elements of one CTA
-constexpr int kGroups = 128;     // groups of 4 threads whose maxima bound the k-th largest
+constexpr int kCap = 1024;       // noted batches of one CTA, and elements collected from them
+constexpr int kGroups = 128;     // groups of 2 threads whose maxima bound the k-th largest
 constexpr int kMaxCluster = 8;
 constexpr float kFar = -1e4f;    // exp2 of it and of anything below is 0; keeps 0 * d finite
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -119,46 +124,117 @@ __device__ __forceinline__ Stat join_lanes(Stat st, float c) {
   return st;
 }
 
-// Adds one or eight elements whose largest is mx (NaN if one is).
-template <int N>
-__device__ __forceinline__ void add(Stat& st, const float (&v)[N], float mx, float c) {
-  raise(st, mx, c);
-  const float mc = __fmul_rn(st.m, c);
-  float s1 = 0.f, t1 = 0.f;
-  if (near(st.m, c)) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      // (-inf: p = exp2(kFar) = 0, with a finite product)
-      const float d = max_nan(fmaf(v[e], c, -mc), kFar), p = exp2_approx(d);
-      if (e & 1) {
-        s1 += p;
-        t1 = fmaf(p, d, t1);
-      } else {
-        st.s += p;
-        st.t = fmaf(p, d, st.t);
-      }
+// Two fp32 numbers in a 64-bit register, for the packed instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A thread's running statistics: those of Stat with separate sums for even and odd elements.
+struct Running {
+  float m = -INFINITY, c, mc = 0.f;  // mc: m c rounded
+  bool is_near = false;
+  uint64_t s = 0, t = 0;
+  __device__ __forceinline__ explicit Running(float c_) : c(c_) {}
+  __device__ __forceinline__ Stat stat() const {
+    const float2 a = unpair(s), b = unpair(t);
+    return {m, a.x + a.y, b.x + b.y};
+  }
+  // Elements whose largest is mx (NaN if one is): first see, then add them.
+  __device__ __forceinline__ void see(float mx) {
+    if (mx > m) {
+      Stat a = stat();
+      raise(a, mx, c);
+      m = mx;
+      mc = __fmul_rn(m, c);
+      is_near = near(m, c);
+      s = pair(a.s, 0.f);
+      t = pair(a.t, 0.f);
     }
-  } else {
+  }
+  template <int N>
+  __device__ __forceinline__ void add_near(const float (&v)[N]) {
+    const uint64_t cc = pair(c, c), mm = pair(-mc, -mc);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (v[e] != -INFINITY) {
-        const float d = max_nan((v[e] - st.m) * c, kFar), p = exp2_approx(d);
-        st.s += p;
-        st.t = fmaf(p, d, st.t);
+    for (int e = 0; e < N; e += 2) {
+      const float2 d = unpair(fma2(pair(v[e], v[e + 1]), cc, mm));
+      // (-inf: p = exp2(kFar) = 0, with a finite product)
+      const float x = max_nan(d.x, kFar), y = max_nan(d.y, kFar);
+      const uint64_t p = pair(exp2_approx(x), exp2_approx(y));
+      s = add2(s, p);
+      t = fma2(p, pair(x, y), t);
+    }
+  }
+  __device__ __forceinline__ void add(float v) {
+    if (v != -INFINITY) {
+      const float d = max_nan(is_near ? fmaf(v, c, -mc) : (v - m) * c, kFar), p = exp2_approx(d);
+      s = add2(s, pair(p, 0.f));
+      t = fma2(pair(p, 0.f), pair(d, 0.f), t);
+    }
+  }
+};
+
+// A batch of a thread's steps (8 elements each) as they lie in memory: 64 bytes.
+template <typename T>
+struct Batch {
+  static constexpr int kSteps = sizeof(T) == 2 ? 4 : 2;
+  Raw8<T> w[kSteps];
+  // Steps at, at + kThreads, ... of `steps`; -inf behind the last.
+  __device__ __forceinline__ void load(const T* body, int at, int steps) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (at + i * kThreads < steps) {
+        w[i].load(body + static_cast<int64_t>(at + i * kThreads) * 8);
+      } else {
+        float none[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) none[e] = -INFINITY;
+        w[i].pack(none);
       }
     }
   }
-  st.s += s1;
-  st.t += t1;
-}
-
-template <int N>
-__device__ __forceinline__ float largest(const float (&v)[N]) {
-  float m = v[0];
+  // The largest element, NaN if there is one: two at a time for the 16-bit types.
+  __device__ __forceinline__ float largest() const {
+    if constexpr (sizeof(T) == 2) {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      T2 m = *reinterpret_cast<const T2*>(&w[0].w.x);
 #pragma unroll
-  for (int e = 1; e < N; ++e) m = max_nan(m, v[e]);
-  return m;
-}
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t u[4] = {w[i].w.x, w[i].w.y, w[i].w.z, w[i].w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = __hmax2_nan(m, *reinterpret_cast<const T2*>(&u[e]));
+      }
+      const float2 f = unpack2<T>(*reinterpret_cast<const uint32_t*>(&m));
+      return max_nan(f.x, f.y);
+    } else {
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        float v[8];
+        w[i].unpack(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_nan(m, v[e]);
+      }
+      return m;
+    }
+  }
+};
 
 struct FwdArgs {
   const void* logits;
@@ -176,10 +252,11 @@ struct Shared {
   Stat peers[kMaxCluster];                                  // first CTA: every CTA's statistics
   unsigned long long top[kMaxCluster * kMaxTop];            // first CTA: every CTA's top entries
   unsigned long long best[kThreads / 32];                   // one round of the slow selection
+  unsigned long long noted[kCap];                           // batches that reach the bound: (key of the largest, first step)
   unsigned long long found[kCap];
   __align__(16) uint32_t group[kGroups];
   uint32_t bound;
-  int count;
+  int batches, count;  // noted and found (counted on beyond the space)
 };
 
 // Element range [begin, end) of a row for a thread's loop: f(index, value) once for each element,
@@ -203,12 +280,11 @@ __device__ __forceinline__ void each(const T* row, int begin, int end, F8&& f8, 
   if (tail + static_cast<int>(threadIdx.x) < end) f1(tail + threadIdx.x, to_f32(row[tail + threadIdx.x]));
 }
 
-// The `top`-th largest of the maxima of the CTA's groups of 4 threads, as a key (0 while
+// The `top`-th largest of the maxima of the CTA's groups of 2 threads, as a key (0 while
 // fewer groups have seen an element).  `mx`: this thread's largest key, 0 for none.
 __device__ __forceinline__ uint32_t bound_of(Shared& S, uint32_t mx, int top) {
   mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  if ((threadIdx.x & 3) == 0) S.group[threadIdx.x >> 2] = mx;
+  if ((threadIdx.x & 1) == 0) S.group[threadIdx.x >> 1] = mx;
   if (threadIdx.x == 0) S.bound = 0;
   __syncthreads();
   if (threadIdx.x < kGroups) {
@@ -243,7 +319,7 @@ __device__ __forceinline__ void order_entries(const unsigned long long* from, in
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) token_logprobs_fwd_kernel(const FwdArgs a) {
   __shared__ Shared S;
   uint32_t rank, peers;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -256,13 +332,13 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const F
   const int end = static_cast<int>(min(static_cast<int64_t>(begin) + part, static_cast<int64_t>(a.vocab)));
   const int top = min(a.top, end - begin);  // this part's share of the candidates
   const float scale = a.scale, c2 = a.c;
-  if (threadIdx.x == 0) S.count = 0;
+  if (threadIdx.x == 0) S.count = S.batches = 0;
   // (awaited before the first access to another CTA's shared memory: that CTA has started by then)
   if (peers > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // the part as [head][body: 16-byte aligned, 8 elements a step][tail]; every thread has one element of head
   // and tail at most
-  Stat st = {-INFINITY, 0.f, 0.f};
+  Running run(c2);
   const bool want = top > 0;
   const int head = min(end - begin, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(row + begin) & 15u)) & 15u) / sizeof(T)));
   const int steps = (end - begin - head) / 8, ends = end - begin - steps * 8;
@@ -270,51 +346,58 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const F
   const bool has_end = static_cast<int>(threadIdx.x) < ends;
   const int end_at = begin + static_cast<int>(threadIdx.x) + (static_cast<int>(threadIdx.x) < head ? 0 : steps * 8);
   float edge[1] = {-INFINITY};
-  if (has_end) edge[0] = to_f32(row[end_at]);
 
-  constexpr int kBatch = 4;  // steps whose loads are in flight together
-  Raw8<T> w[kBatch];
-  auto load = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (at + i * kThreads < steps) w[i].load(body + static_cast<int64_t>(at + i * kThreads) * 8);
-  };
-  load(threadIdx.x);
-  uint32_t bound = 0;
-  float bound_value = -INFINITY;  // (NaN: only NaNs reach it)
-  if (want) {                     // the bound on the top entries from the first batch
-    uint32_t mx = has_end ? order_key(edge[0]) : 0u;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (static_cast<int>(threadIdx.x) + i * kThreads < steps) {
-        float v[8];
-        w[i].unpack(v);
-        mx = max(mx, order_key(largest(v)));
-      }
-    bound = bound_of(S, mx, top);
+  using B = Batch<T>;
+  B now;
+  now.load(body, threadIdx.x, steps);
+  if (has_end) edge[0] = to_f32(row[end_at]);
+  uint32_t bound = 0, most = has_end ? order_key(edge[0]) : 0u;  // most: this thread's largest
+  float bound_value = -INFINITY;                                 // (NaN: only NaNs reach it)
+  if (want) {  // the bound on the top entries, from the threads' first batches
+    if (static_cast<int>(threadIdx.x) < steps) most = max(most, order_key(now.largest()));
+    bound = bound_of(S, most, top);
     if (bound) bound_value = key_value(bound);
   }
   if (has_end) {
-    add(st, edge, edge[0], c2);
-    if (want && order_key(edge[0]) >= bound) collect(S, order_key(edge[0]), end_at);
+    run.see(edge[0]);
+    run.add(edge[0]);
   }
-  for (int at = threadIdx.x; at < steps; at += kBatch * kThreads) {
-    if (at != static_cast<int>(threadIdx.x)) load(at);
+  constexpr int kStride = B::kSteps * kThreads;
+#pragma unroll 1
+  for (int at = threadIdx.x; at < steps; at += kStride) {
+    B next;
+    next.load(body, at + kStride, steps);
+    const float mx = now.largest();
+    run.see(mx);
+    if (run.is_near) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (at + i * kThreads < steps) {
+      for (int i = 0; i < B::kSteps; ++i) {
         float v[8];
-        w[i].unpack(v);
-        const float mx = largest(v);
-        add(st, v, mx, c2);
-        if (want && !(mx < bound_value))
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t k = order_key(v[e]);
-            if (k >= bound) collect(S, k, begin + head + (at + i * kThreads) * 8 + e);
-          }
+        now.w[i].unpack(v);
+        run.add_near(v);
       }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < B::kSteps; ++i) {
+        float v[8];
+        if (at + i * kThreads < steps) {
+          Raw8<T> w;
+          w.load(body + static_cast<int64_t>(at + i * kThreads) * 8);
+          w.unpack(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) run.add(v[e]);
+        }
+      }
+    }
+    if (want && !(mx < bound_value)) {
+      const uint32_t key = order_key(mx);
+      most = max(most, key);
+      const int note = atomicAdd(&S.batches, 1);
+      if (note < kCap) S.noted[note] = (static_cast<unsigned long long>(key) << 32) | static_cast<uint32_t>(at);
+    }
+    now = next;
   }
+  Stat st = run.stat();
 
   // statistics of the CTA
   st = join_lanes(st, c2);
@@ -323,34 +406,32 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const F
 
   // this part's top entries, in order, into the first CTA's shared memory
   if (want) {
-    int n = S.count;
     unsigned long long* mine = S.top;
-    if (n > kCap) {  // uniform: the bound of the whole part
-      uint32_t mx = 0;
-      each(row, begin, end,
-           [&](int, const float (&v)[8]) {
-#pragma unroll
-             for (int e = 0; e < 8; ++e) mx = max(mx, order_key(v[e]));
-           },
-           [&](int, float v) { mx = max(mx, order_key(v)); });
-      __syncthreads();
-      if (threadIdx.x == 0) S.count = 0;
-      bound = bound_of(S, mx, top);
+    bound = bound_of(S, most, top);
+    const int notes = S.batches;
+    auto consider = [&](float v, int index) {
+      const uint32_t k = order_key(v);
+      if (k >= bound) collect(S, k, index);
+    };
+    if (has_end && notes <= kCap) consider(edge[0], end_at);
+    if (notes <= kCap) {
+      constexpr int kEach = B::kSteps * 8;
+      for (int i = threadIdx.x; i < notes * kEach; i += kThreads) {
+        const unsigned long long note = S.noted[i / kEach];
+        if (static_cast<uint32_t>(note >> 32) < bound) continue;
+        const int step = static_cast<int>(static_cast<uint32_t>(note)) + i % kEach / 8 * kThreads;
+        if (step < steps) consider(to_f32(body[static_cast<int64_t>(step) * 8 + i % 8]), begin + head + step * 8 + i % 8);
+      }
+    } else {  // uniform
       each(row, begin, end,
            [&](int c, const float (&v)[8]) {
 #pragma unroll
-             for (int e = 0; e < 8; ++e) {
-               const uint32_t k = order_key(v[e]);
-               if (k >= bound) collect(S, k, c + e);
-             }
+             for (int e = 0; e < 8; ++e) consider(v[e], c + e);
            },
-           [&](int c, float v) {
-             const uint32_t k = order_key(v);
-             if (k >= bound) collect(S, k, c);
-           });
-      __syncthreads();
-      n = S.count;
+           [&](int c, float v) { consider(v, c); });
     }
+    __syncthreads();
+    const int n = S.count;
     if (n <= kCap) {
       order_entries(S.found, n, top, mine);
     } else {  // one pass per entry: the largest below the last one
@@ -381,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_fwd_kernel(const F
     }
   }
   if (threadIdx.x < 32) {
-    st = threadIdx.x < kThreads / 32 ? S.stat[threadIdx.x] : Stat{-INFINITY, 0.f, 0.f};
+    st = static_cast<int>(threadIdx.x) < kThreads / 32 ? S.stat[threadIdx.x] : Stat{-INFINITY, 0.f, 0.f};
     st = join_lanes(st, c2);
   }
   __syncthreads();
@@ -527,13 +608,13 @@ bconv_status_t check_desc(const bconv_token_desc_t* d) {
 
 template <typename T>
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
-  // CTAs per row: those that finish first, at two CTAs an SM, a CTA's fixed cost (the bound, the joins) being
-  // that of some 12000 elements (3 us)
-  const int64_t slots = 2 * static_cast<int64_t>(current_sm_count());
+  // CTAs per row: those that finish first, a CTA's fixed cost (the bound, the joins) being that of some
+  // 8000 elements
+  const int64_t slots = kCtas * static_cast<int64_t>(current_sm_count());
   unsigned peers = 1;
   double best = 1e300;
   for (unsigned p = 1; p <= kMaxCluster; p *= 2) {
-    const double cost = static_cast<double>(ceil_div(a.rows * p, slots)) * (static_cast<double>(a.vocab) / p + 12000.0);
+    const double cost = static_cast<double>(ceil_div(a.rows * p, slots)) * (static_cast<double>(a.vocab) / p + 8000.0);
     if (cost < best * 0.98) {
       best = cost;
       peers = p;
