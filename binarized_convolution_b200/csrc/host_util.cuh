@@ -3,6 +3,10 @@
 
 #include <cuda_runtime.h>
 
+#include <stdint.h>
+
+#include <atomic>
+
 #include "bconv.h"
 
 namespace bconv {
@@ -29,6 +33,21 @@ inline bconv_status_t from_cuda(cudaError_t e) {
   if (e == cudaErrorMemoryAllocation) return BCONV_ERR_OOM;
   if (e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver) return BCONV_ERR_NO_DEVICE;
   return BCONV_ERR_CUDA;
+}
+
+// Lets the current device run Kern with `bytes` (a constant of the call site) of dynamic shared memory; asked of the
+// runtime once per device.
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace bconv

@@ -101,6 +101,15 @@ namespace {
 
 bool valid(bfc_quant_handle_t h) { return h && h->magic == kQuantMagic; }
 
+QuantFcArgs args_of(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows, void* out, int64_t out_stride) {
+  QuantFcArgs a{};
+  a.codes = h->codes; a.scale = h->scale; a.zero = h->zero; a.bias = h->bias; a.err = h->err;
+  a.in = in; a.in_stride = in_stride; a.rows = rows; a.out = out; a.out_stride = out_stride;
+  a.k = h->desc.in_channels; a.no = h->desc.out_channels; a.no_pad = h->no_pad;
+  a.k_tiles = h->k_tiles; a.group = h->group; a.relu = h->desc.neuron == BCONV_NEURON_RELU;
+  return a;
+}
+
 cudaError_t fill(bfc_quant_handle_s* h, const uint8_t* codes, const float* scale, const uint8_t* zero,
                  const float* bias) {
   const int k = h->desc.in_channels, no = h->desc.out_channels;
@@ -190,7 +199,9 @@ bconv_status_t bfc_quant_create(const bfc_quant_desc_t* d, const uint8_t* codes,
 
 int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows) {
   if (!valid(h) || rows < 0 || rows > kMaxRows || in_stride < h->desc.in_channels) return -1;
-  if (rows == 0 || quant_fc_tma_reads(in, in_stride, h->desc.in_channels, h->desc.in_dtype)) return 0;
+  if (rows == 0 || quant_fc_tma_reads(in, in_stride, h->desc.in_channels, h->desc.in_dtype) ||
+      quant_fc_rows_serves(args_of(h, in, in_stride, rows, nullptr, 0), h->desc.in_dtype))
+    return 0;
   return quant_fc_tc_workspace(rows, h->desc.in_channels, h->desc.in_dtype);
 }
 
@@ -204,9 +215,9 @@ bconv_status_t bfc_quant_forward(bfc_quant_handle_t h, const void* in, int64_t i
   if (!in || !out || (!workspace && bfc_quant_workspace_bytes(h, in, in_stride, rows) > 0)) return BCONV_ERR_INVALID_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return BCONV_ERR_CUDA;
-  QuantFcArgs a{h->codes,  h->scale, h->zero,           h->bias,              in,        out,        h->err,  in_stride,
-                out_stride, rows,    h->desc.in_channels, h->desc.out_channels, h->no_pad, h->k_tiles, h->group,
-                h->desc.neuron == BCONV_NEURON_RELU};
+  const QuantFcArgs a = args_of(h, in, in_stride, rows, out, out_stride);
+  if (quant_fc_rows_serves(a, h->desc.in_dtype))
+    return from_cuda(launch_quant_fc_rows(a, h->desc.in_dtype, h->desc.out_dtype, stream));
   return from_cuda(launch_quant_fc_tc(a, h->desc.in_dtype, h->desc.out_dtype, workspace, stream));
 }
 

@@ -33,6 +33,23 @@ struct QuantFcArgs {
   int relu;
 };
 
+// Codes less zeros: `v` two 4-bit numbers in the halves of a word, or-ed into 1024.0 (fp16) or 128.0 (bf16), whose
+// last significant bits are worth 1; `zero` that constant plus the zero, twice.  Exact.
+template <bool HALF>
+__device__ __forceinline__ uint32_t decode(uint32_t v, uint32_t zero) {
+  const uint32_t a = v | (HALF ? 0x64006400u : 0x43004300u);
+  if (HALF) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&zero));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&zero));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// At most 16 rows that fit in shared memory.
+bool quant_fc_rows_serves(const QuantFcArgs& q, int in_dtype);
+cudaError_t launch_quant_fc_rows(const QuantFcArgs& q, int in_dtype, int out_dtype, cudaStream_t s);
 // Whether the tensor-core kernel reads these rows as they are (else they are staged in the workspace,
 // of quant_fc_tc_workspace bytes).
 bool quant_fc_tma_reads(const void* in, int64_t in_stride, int k, int in_dtype);

@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "host_util.cuh"
 #include "quant_fc.cuh"
 #include "tc_device.cuh"
 
@@ -187,17 +188,6 @@ __device__ __forceinline__ void drain(uint64_t* full, int stages, int issued) {
   for (int i = max(0, issued - stages); i < issued; ++i)
     while (!mbar_try_suspend(&full[i % stages], static_cast<uint32_t>(i / stages) & 1u, 20000u))
       if (globaltimer() - t0 > kTimeoutNs) return;
-}
-
-template <bool HALF>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  if (HALF) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Four channels of a token, of which `left` are the layer's.
@@ -457,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < 4; ++p)
               v[c * 16 + t * 4 + p] =
-                  sub2<HALF>(((w[t][2 * two + c] >> (4 * p)) & 0x000f000fu) | (kBias * 0x10001u), zz[2 * two + c]);
+                  decode<HALF>((w[t][2 * two + c] >> (4 * p)) & 0x000f000fu, zz[2 * two + c]);
         if (two == 0) {  // the stage is free when the MMAs of tile i - 2 are done
           if (i >= 2) {
             ok = wait_warp(done + 8 * ds, dph, B, err);
@@ -691,7 +681,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 template <int HALVES, bool HALF, int UNITS>
 cudaError_t launch(const CUtensorMap& map, const TcQuantArgs& a, int64_t tiles, cudaStream_t s) {
   auto kern = quant_fc_tc_kernel<HALVES, HALF, UNITS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = allow_smem<quant_fc_tc_kernel<HALVES, HALF, UNITS>>(kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
