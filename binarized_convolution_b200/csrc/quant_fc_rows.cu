@@ -64,46 +64,69 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr uint32_t kBias = HALF ? 0x6400u : 0x4300u;  // 1024.0 or 128.0: or-ing a 4-bit number in adds it
   constexpr int kDepth = UNITS == 1 ? 4 : 2;
-  constexpr int kGroup = kQuantK / UNITS;
-  extern __shared__ __align__(16) uint8_t smem[];  // [part][row][pitch]
+  extern __shared__ __align__(16) uint8_t smem[];  // [part][row][pitch], 256 bytes of zeros
   __shared__ float sums[kWarps][NT * 4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = static_cast<int>(a.q.rows);
   const int share = warp % a.ksplit, team = warp / a.ksplit, teams = kWarps / a.ksplit;
-  const int groups = (a.q.k + a.q.group - 1) / a.q.group;
   const int kt0 = min(share * a.k_each, a.q.k_tiles), nk = min(kt0 + a.k_each, a.q.k_tiles) - kt0;
 
-  // items: tile after tile, nk steps each
+  // items: tile after tile, nk steps each.  The addresses of the next one to load move on by additions.
   const int stride = gridDim.x * teams, first = blockIdx.x * teams + team;
   Item<UNITS> ring[kDepth];
-  int l_tile = first, l_k = 0;  // the next item to load
+  int l_tile = first, l_k = 0, l_group = 0, l_left = 0;  // l_left: steps until the next group (one unit)
+  const uint4* l_codes = nullptr;
+  int64_t l_terms = 0;  // of the scales and zeros
+  const int last_group = (a.q.k + a.q.group - 1) / a.q.group - 1;
+  const int steps_per_group = a.q.group / kQuantK;  // (one unit)
+  auto start_tile = [&]() {
+    const int row = l_tile * 16 + g;
+    l_codes = a.q.codes + (static_cast<int64_t>(row / kQuantRows) * a.q.k_tiles + kt0) * (kQuantTileBytes / 16) +
+              t * kQuantRows + row % kQuantRows;
+    l_group = UNITS == 1 ? kt0 / steps_per_group : kt0 * UNITS;
+    l_left = UNITS == 1 ? steps_per_group - (kt0 - l_group * steps_per_group) : 0;
+    l_terms = static_cast<int64_t>(min(l_group, last_group)) * a.q.no_pad + row;
+  };
   auto load = [&](Item<UNITS>& it) {
-    if (nk == 0 || l_tile >= a.tiles) return;
-    const int row = l_tile * 16 + g, rt = row / kQuantRows, in = row % kQuantRows, kt = kt0 + l_k;
-    const uint4* from = a.q.codes + (static_cast<int64_t>(rt) * a.q.k_tiles + kt) * (kQuantTileBytes / 16) + t * kQuantRows + in;
-    it.w[0] = __ldcs(from);
-    it.w[1] = __ldcs(from + 8);
+    if (l_tile >= a.tiles) return;
+    it.w[0] = __ldcs(l_codes);
+    it.w[1] = __ldcs(l_codes + 8);
+    l_codes += kQuantTileBytes / 16;
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
+      it.s[0][u] = __ldg(a.q.scale + l_terms);
+      it.s[1][u] = __ldg(a.q.scale + l_terms + 8);
+      if (a.q.zero) {
+        it.z[0][u] = a.q.zero[l_terms];
+        it.z[1][u] = a.q.zero[l_terms + 8];
+      }
       // (behind the last group the inputs are 0)
-      const int64_t at = static_cast<int64_t>(min((kt * kQuantK + u * kGroup) / a.q.group, groups - 1)) * a.q.no_pad + row;
-      it.s[0][u] = __ldg(a.q.scale + at);
-      it.s[1][u] = __ldg(a.q.scale + at + 8);
-      it.z[0][u] = a.q.zero ? a.q.zero[at] : 8u;
-      it.z[1][u] = a.q.zero ? a.q.zero[at + 8] : 8u;
+      if (UNITS > 1 || --l_left == 0) {
+        if (l_group++ < last_group) l_terms += a.q.no_pad;
+        l_left = steps_per_group;
+      }
     }
     if (++l_k == nk) {
       l_k = 0;
       l_tile += stride;
+      start_tile();
     }
   };
+  if (nk == 0) l_tile = a.tiles;
+  start_tile();
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i)
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) ring[i].z[0][u] = ring[i].z[1][u] = 8u;
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) load(ring[i]);
 
   // the rows into shared memory, 8 channels at a time, channels behind the last as 0
+  const int plane = rows * a.pitch;
+  if (threadIdx.x < 16) *reinterpret_cast<uint4*>(smem + PARTS * plane + threadIdx.x * 16) = make_uint4(0u, 0u, 0u, 0u);
   wait_prior_grid();
   {
-    const int octets = a.q.k_tiles * (kQuantK / 8), total = rows * octets, plane = rows * a.pitch;
+    const int octets = a.q.k_tiles * (kQuantK / 8), total = rows * octets;
     const bool vec = (reinterpret_cast<uintptr_t>(a.q.in) & 15u) == 0 && a.q.in_stride % 8 == 0;
     constexpr int kBatch = 4;  // loads in flight together
     for (int base = threadIdx.x; base < total; base += kBatch * kThreads) {
@@ -151,7 +174,15 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   const int turns = (a.tiles - static_cast<int>(blockIdx.x) * teams + stride - 1) / stride;  // of the CTA's first team
   int tile = first, k = 0;
-  const uint8_t* x_at = smem + g * a.pitch + (kt0 * kQuantK + 8 * t) * 2;
+  // this lane's B operands: row n * 8 + g, or zeros (256 bytes behind the rows) where there is no such row
+  const uint8_t *x_start[NT], *x_at[NT];
+  int x_step[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool real = n * 8 + g < rows;
+    x_start[n] = x_at[n] = real ? smem + (n * 8 + g) * a.pitch + (kt0 * kQuantK + 8 * t) * 2 : smem + PARTS * rows * a.pitch + 16 * t;
+    x_step[n] = real ? kQuantK * 2 : 0;
+  }
 
   auto finish = [&]() {  // the tile's sums are complete (nothing in warps without input channels)
     const bool real = tile < a.tiles;
@@ -188,9 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
     tile += stride;
   };
 
-  auto step = [&](const Item<UNITS>& it, int kk) {
+  auto step = [&](const Item<UNITS>& it) {
     const uint32_t w[2][4] = {{it.w[0].x, it.w[0].y, it.w[0].z, it.w[0].w}, {it.w[1].x, it.w[1].y, it.w[1].z, it.w[1].w}};
-    const uint8_t* xk = x_at + kk * (kQuantK * 2);
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const uint32_t zz[2] = {(kBias | it.z[0][u]) * 0x10001u, (kBias | it.z[1][u]) * 0x10001u};
@@ -211,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            uint4 b = make_uint4(0u, 0u, 0u, 0u);
-            if (n * 8 + g < rows) b = *reinterpret_cast<const uint4*>(xk + (part * rows + n * 8) * a.pitch + c * 64);
+            const uint4 b = *reinterpret_cast<const uint4*>(x_at[n] + (x_step[n] ? part * plane : 0) + c * 64);
             mma16816<HALF>(d[n], a0, b.x, b.y);
             mma16816<HALF>(d[n], a1, b.z, b.w);
           }
@@ -235,10 +264,14 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) {
       if (done < turns) {
-        step(ring[i], k);
+        step(ring[i]);
         load(ring[i]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x_at[n] += x_step[n];
         if (++k == nk) {
           k = 0;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x_at[n] = x_start[n];
           finish();
           ++done;
         }
@@ -260,7 +293,7 @@ cudaError_t launch(const RowsArgs& a, int out_dtype, int ctas, int smem, cudaStr
 // bytes) meet different banks.
 int pitch_for(const QuantFcArgs& q) { return round_up(q.k_tiles * kQuantK * 2, 128) + 64; }
 int smem_for(const QuantFcArgs& q, int in_dtype) {
-  return pitch_for(q) * static_cast<int>(q.rows) * (in_dtype == BCONV_DTYPE_F32 ? 3 : 1);
+  return pitch_for(q) * static_cast<int>(q.rows) * (in_dtype == BCONV_DTYPE_F32 ? 3 : 1) + 256;
 }
 
 }  // namespace
