@@ -9,9 +9,10 @@ copied.  Gradients are explicit calls; nothing here records for autograd.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import NamedTuple
 
-import ctypes
 import torch
 
 from . import _native as nat
@@ -28,17 +29,29 @@ def _dtype(t) -> torch.dtype:
     return t
 
 
-def _on(x):
-    """A context that makes x's device current (nothing to do, and nothing spent, when it is)."""
-    return torch.cuda.device(x.device)
+# The calls below are as short as the kernels they launch, so the checks are few and cheap: integers instead of
+# torch.device objects, the C functions directly.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty_like = torch.empty_like
+_F32 = torch.float32
 
 
-def _stream(x) -> int:
-    return torch._C._cuda_getCurrentRawStream(x.device.index)
+def _call(name, device, *args):
+    """A C entry point on the current stream of the device."""
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(nat.load_library(), name)
+    if device == _current_device():
+        status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
+    if status:
+        raise nat.BconvError(status, name)
 
 
-def _is_current(x) -> bool:
-    return x.device.index == torch.cuda.current_device()
+_FUNCTIONS: dict = {}
 
 
 def _activation(x, name):
@@ -49,17 +62,15 @@ def _activation(x, name):
     return x
 
 
-def _like(t, ref, shape, name, dtype=None):
-    """t as a contiguous tensor, checked against ref's device, the dtype and the shape; None stays None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.device != ref.device:
-        raise TypeError(f"{name}: expected a tensor on {ref.device}")
-    if t.dtype != (dtype or ref.dtype):
-        raise TypeError(f"{name}: expected {dtype or ref.dtype}, got {t.dtype}")
+def _like(t, device, dtype, shape, name):
+    """t as a contiguous tensor, checked against a device, a dtype and a shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError(f"{name}: expected a tensor on cuda:{device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _ptr(t):
@@ -68,8 +79,10 @@ def _ptr(t):
 
 def _rows(x):
     """(tensor, rows, row stride) of x as a matrix over its last dimension; copied if it is none."""
-    if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]:
-        return x, x.shape[0], x.stride(0)
+    if x.dim() == 2:
+        stride = x.stride()
+        if stride[1] == 1 and stride[0] >= x.shape[1]:
+            return x, x.shape[0], stride[0]
     x = x.contiguous()
     width = x.shape[-1]
     return x, x.numel() // width if width else 0, width
@@ -117,6 +130,9 @@ class QuantFC(_Layer):
                                     _DTYPES[self.out_dtype])
         self.handle = nat.bfc_quant_create(desc, _ptr(packed), _ptr(scale), _ptr(zero), _ptr(bias))
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._device = self.device.index
+        lib = nat.load_library()
+        self._forward, self._workspace_bytes = lib.bfc_quant_forward, lib.bfc_quant_workspace_bytes
 
     @staticmethod
     def _array(a, dtype, shape, name):
@@ -149,9 +165,11 @@ class QuantFC(_Layer):
 
     def forward_into(self, x, out):
         """x [..., in_channels] into out [..., out_channels] (the rows of out may be strided)."""
-        if self.handle is None:
+        handle, device = self.handle, self._device
+        if handle is None:
             raise ValueError("the layer is closed")
-        if not isinstance(x, torch.Tensor) or x.device != self.device or out.device != self.device:
+        if (not isinstance(x, torch.Tensor) or not isinstance(out, torch.Tensor) or x.get_device() != device
+                or out.get_device() != device):
             raise TypeError(f"expected tensors on {self.device}")
         if x.dtype != self.dtype or out.dtype != self.out_dtype:
             raise TypeError(f"expected {self.dtype} -> {self.out_dtype}, got {x.dtype} -> {out.dtype}")
@@ -160,12 +178,15 @@ class QuantFC(_Layer):
                              f"{tuple(x.shape)} -> {tuple(out.shape)}")
         x, rows, in_stride = _rows(x)
         to, _, out_stride = _rows(out)
-        if to.data_ptr() != out.data_ptr():
+        if to is not out and to.data_ptr() != out.data_ptr():
             raise ValueError("out must have contiguous channels, and rows without gaps unless it is a matrix")
-        need = nat.bfc_quant_workspace_bytes(self.handle, x.data_ptr(), in_stride, rows)
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need > 0 else None
-        nat.bfc_quant_forward(self.handle, x.data_ptr(), in_stride, rows, to.data_ptr(), out_stride, _ptr(ws),
-                              _stream(x))
+        at = x.data_ptr()
+        need = self._workspace_bytes(handle, at, in_stride, rows)
+        ws = x.new_empty(need, dtype=torch.uint8) if need > 0 else None
+        # (the library makes the layer's device current itself)
+        status = self._forward(handle, at, in_stride, rows, to.data_ptr(), out_stride, _ptr(ws), _raw_stream(device))
+        if status:
+            raise nat.BconvError(status, "bfc_quant_forward")
         return out
 
     def __call__(self, x):
@@ -173,16 +194,12 @@ class QuantFC(_Layer):
             raise TypeError("expected a CUDA tensor")
         if x.dim() < 1:
             raise ValueError("expected [..., in_channels]")
-        out = torch.empty(x.shape[:-1] + (self.out_channels,), dtype=self.out_dtype, device=x.device)
+        out = x.new_empty(x.shape[:-1] + (self.out_channels,), dtype=self.out_dtype)
         return self.forward_into(x, out)
 
     def sync_status(self):
-        with torch.cuda.device(self.device):
-            nat.bfc_quant_sync_status(self.handle, _stream_of(self.device))
-
-
-def _stream_of(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+        """Waits for the current stream of the layer's device and raises if a kernel of the layer gave up a wait."""
+        nat.bfc_quant_sync_status(self.handle, _raw_stream(self._device))
 
 
 class BlockNorm(NamedTuple):
@@ -198,17 +215,29 @@ class BlockNormGrad(NamedTuple):
     d_gate: torch.Tensor | None
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_desc(rows, per, width, dtype, residual_scale, eps):
+    desc = nat.bconv_block_norm_desc_t(rows, per, width, _DTYPES[dtype], residual_scale, eps)
+    return desc, ctypes.byref(desc), nat.load_library().bconv_block_norm_workspace_bytes(desc)
+
+
 def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps):
-    residual = _activation(residual, "residual").contiguous()
-    if residual.dim() < 1 or residual.shape[-1] == 0:
+    residual = _activation(residual, "residual")
+    if not residual.is_contiguous():
+        residual = residual.contiguous()
+    shape, dtype, device = residual.shape, residual.dtype, residual.get_device()
+    if not shape or shape[-1] == 0:
         raise ValueError("residual: expected [..., width]")
-    width = residual.shape[-1]
+    width = shape[-1]
     rows = residual.numel() // width
-    block = _like(block, residual, residual.shape, "block")
-    pre_weight = _like(pre_weight, residual, (width,), "pre_weight", torch.float32)
-    post_weight = _like(post_weight, residual, (width,), "post_weight", torch.float32)
-    if block is None and (gate is not None or post_weight is not None):
+    if block is not None:
+        block = _like(block, device, dtype, shape, "block")
+    elif gate is not None or post_weight is not None:
         raise ValueError("gate and post_weight belong to a block")
+    if pre_weight is not None:
+        pre_weight = _like(pre_weight, device, _F32, (width,), "pre_weight")
+    if post_weight is not None:
+        post_weight = _like(post_weight, device, _F32, (width,), "post_weight")
     per = 1
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() < 1 or gate.shape[-1] != width:
@@ -220,9 +249,8 @@ def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_ga
         per = max(per, 1)
         if gates != -(-rows // per):
             raise ValueError(f"{gates} gate rows of {per} rows each do not fit {rows} rows")
-        gate = _like(gate, residual, gate.shape, "gate")
-    desc = nat.bconv_block_norm_desc_t(rows, per, width, _DTYPES[residual.dtype], residual_scale, eps)
-    return residual, block, pre_weight, post_weight, gate, desc
+        gate = _like(gate, device, dtype, gate.shape, "gate")
+    return residual, block, pre_weight, post_weight, gate, device, (rows, per, width, dtype, residual_scale, eps)
 
 
 def block_norm(residual, block=None, *, pre_weight=None, post_weight=None, gate=None, rows_per_gate=None,
@@ -239,19 +267,12 @@ def block_norm(residual, block=None, *, pre_weight=None, post_weight=None, gate=
     if block is None and pre_weight is None:
         raise ValueError("without a block there is only the norm: give pre_weight")
     given = residual
-    residual, block, pre_weight, post_weight, gate, desc = _block_norm_args(
+    residual, block, pre_weight, post_weight, gate, device, args = _block_norm_args(
         residual, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps)
-    if not _is_current(residual):
-        with _on(residual):
-            return _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc)
-    return _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc)
-
-
-def _block_norm_run(given, residual, block, pre_weight, post_weight, gate, desc):
-    out = torch.empty_like(residual) if block is not None else None
-    normed = torch.empty_like(residual) if pre_weight is not None else None
-    nat.bconv_block_norm_forward(desc, _ptr(residual), _ptr(block), _ptr(gate), _ptr(post_weight), _ptr(pre_weight),
-                                 _ptr(out), _ptr(normed), _stream(residual))
+    out = _empty_like(residual) if block is not None else None
+    normed = _empty_like(residual) if pre_weight is not None else None
+    _call("bconv_block_norm_forward", device, _norm_desc(*args)[1], residual.data_ptr(), _ptr(block), _ptr(gate),
+          _ptr(post_weight), _ptr(pre_weight), _ptr(out), _ptr(normed))
     return BlockNorm(given if out is None else out, normed)
 
 
@@ -264,31 +285,29 @@ def block_norm_backward(residual_out, block=None, *, pre_weight=None, post_weigh
     residual, block, the weights and the gate (None where the forward had none); the sums
     over rows are float32.
     """
-    residual_out, block, pre_weight, post_weight, gate, desc = _block_norm_args(
+    residual_out, block, pre_weight, post_weight, gate, device, args = _block_norm_args(
         residual_out, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps)
-    d_residual_out = _like(d_residual_out, residual_out, residual_out.shape, "d_residual_out")
-    d_normed = _like(d_normed, residual_out, residual_out.shape, "d_normed")
-    if d_normed is not None and pre_weight is None:
-        raise ValueError("d_normed needs pre_weight")
-    args = (residual_out, block, pre_weight, post_weight, gate, desc, d_residual_out, d_normed)
-    if not _is_current(residual_out):
-        with _on(residual_out):
-            return _block_norm_backward_run(*args)
-    return _block_norm_backward_run(*args)
-
-
-def _block_norm_backward_run(residual_out, block, pre_weight, post_weight, gate, desc, d_residual_out, d_normed):
-    def sums(t):
-        return None if t is None else torch.empty(t.shape, dtype=torch.float32, device=t.device)
-
-    g = BlockNormGrad(torch.empty_like(residual_out), None if block is None else torch.empty_like(block),
-                      sums(pre_weight), sums(post_weight), sums(gate))
-    need = nat.bconv_block_norm_workspace_bytes(desc)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=residual_out.device)
-    nat.bconv_block_norm_backward(desc, _ptr(residual_out), _ptr(block), _ptr(gate), _ptr(post_weight),
-                                  _ptr(pre_weight), _ptr(d_residual_out), _ptr(d_normed), _ptr(g.d_residual),
-                                  _ptr(g.d_block), _ptr(g.d_pre_weight), _ptr(g.d_post_weight), _ptr(g.d_gate),
-                                  _ptr(ws), _stream(residual_out))
+    shape, dtype = residual_out.shape, residual_out.dtype
+    if d_residual_out is not None:
+        d_residual_out = _like(d_residual_out, device, dtype, shape, "d_residual_out")
+    if d_normed is not None:
+        d_normed = _like(d_normed, device, dtype, shape, "d_normed")
+        if pre_weight is None:
+            raise ValueError("d_normed needs pre_weight")
+    g = BlockNormGrad(_empty_like(residual_out), None if block is None else _empty_like(block),
+                      None if pre_weight is None else _empty_like(pre_weight),
+                      None if post_weight is None else _empty_like(post_weight),
+                      None if gate is None else _empty_like(gate, dtype=_F32))
+    if device == _current_device():
+        _, desc, need = _norm_desc(*args)
+    else:  # (the workspace goes by the device's SMs)
+        with torch.cuda.device(device):
+            desc = ctypes.byref(nat.bconv_block_norm_desc_t(*args[:3], _DTYPES[dtype], *args[4:]))
+            need = nat.load_library().bconv_block_norm_workspace_bytes(desc)
+    ws = residual_out.new_empty(max(need, 1), dtype=torch.uint8)
+    _call("bconv_block_norm_backward", device, desc, residual_out.data_ptr(), _ptr(block), _ptr(gate),
+          _ptr(post_weight), _ptr(pre_weight), _ptr(d_residual_out), _ptr(d_normed), g.d_residual.data_ptr(),
+          _ptr(g.d_block), _ptr(g.d_pre_weight), _ptr(g.d_post_weight), _ptr(g.d_gate), ws.data_ptr())
     return g
 
 
@@ -298,6 +317,12 @@ class TokenLogprobs(NamedTuple):
     lse: torch.Tensor
     top_logprob: torch.Tensor | None
     top_index: torch.Tensor | None
+
+
+@functools.lru_cache(maxsize=256)
+def _token_desc(rows, stride, vocab, dtype, top, temperature):
+    desc = nat.bconv_token_desc_t(rows, stride, vocab, _DTYPES[dtype], top, temperature)
+    return desc, ctypes.byref(desc)
 
 
 def _logits(logits):
@@ -314,24 +339,23 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0) -> TokenLogpr
     one outside the vocabulary: NaN).  Returns float32 [...] (``top_logprob`` float32 and ``top_index``
     int32 [..., top], in descending order of the logits, equal ones by ascending index).
     """
-    lead = logits.shape[:-1]
     x, rows, stride = _logits(logits)
-    tokens = _like(tokens, x, lead, "tokens", torch.int64)
-    desc = nat.bconv_token_desc_t(rows, stride, x.shape[-1], _DTYPES[x.dtype], top, temperature)
-    if not _is_current(x):
-        with _on(x):
-            return _token_logprobs_run(x, tokens, lead, top, desc)
-    return _token_logprobs_run(x, tokens, lead, top, desc)
-
-
-def _token_logprobs_run(x, tokens, lead, top, desc):
-    f32 = dict(dtype=torch.float32, device=x.device)
-    r = TokenLogprobs(torch.empty(lead, **f32) if tokens is not None else None, torch.empty(lead, **f32),
-                      torch.empty(lead, **f32), torch.empty(lead + (top,), **f32) if top > 0 else None,
-                      torch.empty(lead + (top,), dtype=torch.int32, device=x.device) if top > 0 else None)
-    nat.bconv_token_logprobs_forward(desc, _ptr(x), _ptr(tokens), _ptr(r.logprob), _ptr(r.entropy), _ptr(r.lse),
-                                     _ptr(r.top_logprob), _ptr(r.top_index), _stream(x))
-    return r
+    lead, device = logits.shape[:-1], x.get_device()
+    if tokens is not None:
+        tokens = _like(tokens, device, torch.int64, lead, "tokens")
+    desc = _token_desc(rows, stride, x.shape[-1], x.dtype, top, temperature)[1]
+    # (one allocation for the statistics of a row)
+    if tokens is not None:
+        logprob, entropy, lse = x.new_empty((3,) + lead, dtype=_F32).unbind(0)
+    else:
+        logprob, (entropy, lse) = None, x.new_empty((2,) + lead, dtype=_F32).unbind(0)
+    top_logprob = top_index = None
+    if top > 0:
+        top_logprob = x.new_empty(lead + (top,), dtype=_F32)
+        top_index = x.new_empty(lead + (top,), dtype=torch.int32)
+    _call("bconv_token_logprobs_forward", device, desc, x.data_ptr(), _ptr(tokens), _ptr(logprob), entropy.data_ptr(),
+          lse.data_ptr(), _ptr(top_logprob), _ptr(top_index))
+    return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, *, d_logprob=None, d_entropy=None, temperature=1.0):
@@ -340,17 +364,21 @@ def token_logprobs_backward(logits, tokens, lse, entropy, *, d_logprob=None, d_e
     lse and entropy are what :func:`token_logprobs` returned for these logits; the result has
     the logits' dtype.  entropy may be None without d_entropy, tokens without d_logprob.
     """
-    lead = logits.shape[:-1]
     x, rows, stride = _logits(logits)
-    tokens = _like(tokens, x, lead, "tokens", torch.int64)
-    lse, entropy, d_logprob, d_entropy = (
-        _like(t, x, lead, name, torch.float32)
-        for t, name in ((lse, "lse"), (entropy, "entropy"), (d_logprob, "d_logprob"), (d_entropy, "d_entropy")))
+    lead, device, vocab = logits.shape[:-1], x.get_device(), x.shape[-1]
     if lse is None or (d_logprob is not None and tokens is None) or (d_entropy is not None and entropy is None):
         raise ValueError("lse is needed, tokens with d_logprob, entropy with d_entropy")
-    desc = nat.bconv_token_desc_t(rows, stride, x.shape[-1], _DTYPES[x.dtype], 0, temperature)
-    with _on(x):
-        out = torch.empty(logits.shape, dtype=x.dtype, device=x.device)
-        nat.bconv_token_logprobs_backward(desc, _ptr(x), _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(d_logprob),
-                                          _ptr(d_entropy), _ptr(out), x.shape[-1], _stream(x))
+    if tokens is not None:
+        tokens = _like(tokens, device, torch.int64, lead, "tokens")
+    lse = _like(lse, device, _F32, lead, "lse")
+    if entropy is not None:
+        entropy = _like(entropy, device, _F32, lead, "entropy")
+    if d_logprob is not None:
+        d_logprob = _like(d_logprob, device, _F32, lead, "d_logprob")
+    if d_entropy is not None:
+        d_entropy = _like(d_entropy, device, _F32, lead, "d_entropy")
+    out = x.new_empty(logits.shape)
+    _call("bconv_token_logprobs_backward", device, _token_desc(rows, stride, vocab, x.dtype, 0, temperature)[1],
+          x.data_ptr(), _ptr(tokens), lse.data_ptr(), _ptr(entropy), _ptr(d_logprob), _ptr(d_entropy), out.data_ptr(),
+          vocab)
     return out
