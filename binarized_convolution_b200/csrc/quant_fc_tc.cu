@@ -137,6 +137,21 @@ __device__ __forceinline__ void ld_wait(uint32_t (&v)[16]) {
                : "memory");
 }
 
+// Two 32-bit registers as one of 64 bits, its halves as fp32, and the packed multiply-add on such pairs.
+__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float half_of(uint64_t p, int high) {
+  return __uint_as_float(static_cast<uint32_t>(high ? p >> 32 : p));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Barriers by their shared-memory address: what a single thread does between two MMAs is on the
 // critical path, instruction by instruction.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -476,9 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int stream = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t from = tmem + static_cast<uint32_t>(2 * stream * kMaxCols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int chunks = a.cols / 16;
-    float acc[kMaxCols];
+    uint64_t acc[kMaxCols / 2];  // pairs of neighbouring tokens, for the packed multiply-add
 #pragma unroll
-    for (int j = 0; j < kMaxCols; ++j) acc[j] = 0.f;
+    for (int j = 0; j < kMaxCols / 2; ++j) acc[j] = 0;
     bool ok = true;
     uint32_t turn = 0, phase = 0;
     const float* scale = reinterpret_cast<const float*>(ring_s) + row;
@@ -492,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t slot = 2u * stream + turn;
       if (!(ok = wait_warp(full_d + 8 * slot, phase, B, err))) break;
       tc_fence_after();
-      const float s = scale[(ss * UNITS + u) * kQuantRows];
+      const uint32_t s = __float_as_uint(scale[(ss * UNITS + u) * kQuantRows]);
+      const uint64_t ss2 = pair_u32(s, s);
       const uint32_t at = from + turn * kMaxCols;
       uint32_t v[2][16];
       ld_16(at, v[0]);
@@ -508,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) arrive(empty_d + 8 * slot);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(s, __uint_as_float(v[c & 1][j]), acc[c * 16 + j]);
+          for (int j = 0; j < 8; ++j)
+            acc[c * 8 + j] = fma_f32x2(ss2, pair_u32(v[c & 1][2 * j], v[c & 1][2 * j + 1]), acc[c * 8 + j]);
         }
       turn ^= 1u;
       if (turn == 0) phase ^= 1u;
@@ -527,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kMaxCols / 16; ++c)
         if (c < chunks) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] = acc[c * 16 + j];
+          for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] = half_of(acc[c * 8 + j / 2], j & 1);
         }
     if (HALVES == 1) {  // the other half of the units
       named_barrier(256);
@@ -536,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kMaxCols / 16; ++c)
           if (c < chunks) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] += acc[c * 16 + j];
+            for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] += half_of(acc[c * 8 + j / 2], j & 1);
           }
     }
     if (a.splits > 1)
