@@ -50,11 +50,10 @@ constexpr int kWStages = 6;          // tiles of codes in flight
 constexpr int kMaxStages = 8;        // tiles of tokens in flight
 constexpr int kScaleSlack = 4;       // the scales of a tile are used up to so many tiles after its tokens
 constexpr int kMaxCols = 96;         // tokens of an MMA
-constexpr int kSlots = 4;            // accumulators of kMaxCols TMEM columns
-constexpr int kAStages = 2;          // decoded tiles, one of each decoding warpgroup
+constexpr int kSlots = 4;            // accumulators
 constexpr int kACols = kQuantK / 2;  // TMEM columns of a decoded tile
-constexpr uint32_t kTmemCols = 512;
-static_assert(kSlots * kMaxCols + kAStages * kACols <= 512, "TMEM");
+constexpr int kTmemCols = 512;
+static_assert(kSlots * kMaxCols + 2 * kACols <= kTmemCols, "TMEM: a decoded tile of each decoding warpgroup at least");
 constexpr int kMaxSplit = 8;
 constexpr int kSmemBytes = 226 * 1024;
 
@@ -74,6 +73,8 @@ constexpr int kRingBytes = (kSmemBytes - static_cast<int>(sizeof(Bars))) / 1024 
 struct TcQuantArgs {
   QuantFcArgs q;
   int cols;        // tokens of an MMA (a multiple of 16, at most kMaxCols)
+  int slot_cols;   // TMEM columns between the accumulators
+  int a_stages;    // decoded tiles in TMEM (even: the decoding warpgroups take turns)
   int parts;       // bf16 parts of the input (3 for fp32)
   int part_rows;   // rows between the parts in the tensor map
   int stages;      // tiles of tokens in flight
@@ -279,14 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem_base)),
-                 "r"(kTmemCols));
+                 "r"(static_cast<uint32_t>(kTmemCols)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_base;
-  const uint32_t tmem_a = tmem + kSlots * kMaxCols;
+  const uint32_t tmem_a = tmem + static_cast<uint32_t>(kSlots * a.slot_cols);
   const int groups = (a.q.k + a.q.group - 1) / a.q.group;
   // first of the tile's channels in a [groups][no_pad] array (behind the last group the inputs are 0)
   auto group_at = [&](int i, int u) {
@@ -341,11 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t desc = desc0, ready_ph = 0;
         // slot: 2 * stream + turn; streams: the halves of the tokens, or every second unit
         uint32_t turn = 0, empty_ph = 1, stream = 0;
-        int s = 0;
+        int s = 0, as = 0;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
           if (!(ok = wait(ready + 8 * s, ready_ph, B, err))) break;
-          const uint32_t a_tmem = tmem_a + static_cast<uint32_t>(i & 1) * kACols;
+          const uint32_t a_tmem = tmem_a + static_cast<uint32_t>(as * kACols);
+          if (++as == a.a_stages) as = 0;
 #pragma unroll
           for (int u = 0; u < UNITS; ++u) {
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t slot = 2u * (HALVES == 2 ? h : stream) + turn;
               if (!ok || !(ok = wait(empty_d + 8 * slot, empty_ph, B, err))) break;
               tc_fence_after();
-              const uint32_t d = tmem + slot * kMaxCols;
+              const uint32_t d = tmem + slot * static_cast<uint32_t>(a.slot_cols);
               for (int p = 0; p < a.parts; ++p) {
                 const uint32_t lo = desc + (HALVES == 2 ? h : p) * desc_piece;
 #pragma unroll
@@ -418,15 +420,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    // ---------------- codes -> operands: tiles odd, odd + 2, ... into the TMEM stage `odd` ----------------
+    // ---------------- codes -> operands: tiles odd, odd + 2, ... ----------------
     const int odd = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t to = tmem_a + static_cast<uint32_t>(odd * kACols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int ws = odd % kWStages;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int ws = odd % kWStages, as = odd;
     uint32_t wph = 0;
-    int s = odd % a.stages;                                    // of tile i
-    int ds = 0;                                                // of tile i - 2
+    int s = odd % a.stages, ds = odd % a.stages;  // of tile i and of tile i - a_stages, whose place it takes
     uint32_t dph = 0;
-    if (odd) ds = 1 % a.stages;
     for (int i = odd; i < n; i += 2) {
       if (!wait_warp(full_w + 8 * ws, wph, B, err)) break;
       const uint8_t* from = ring_w + ws * stage_w + row * 16;
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < 4; ++p)
               v[c * 16 + t * 4 + p] =
                   decode<HALF>((w[t][2 * two + c] >> (4 * p)) & 0x000f000fu, zz[2 * two + c]);
-        if (two == 0) {  // the stage is free when the MMAs of tile i - 2 are done
-          if (i >= 2) {
+        if (two == 0) {  // the place is free when the MMAs of tile i - a_stages are done
+          if (i >= a.a_stages) {
             ok = wait_warp(done + 8 * ds, dph, B, err);
             ds += 2;
             if (ds >= a.stages) {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        st_32x32(to + static_cast<uint32_t>(two * 32), v);
+        st_32x32(tmem_a + lanes + static_cast<uint32_t>(as * kACols + two * 32), v);
       }
       if (!ok) break;
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -484,12 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) arrive(ready + 8 * s);
       s += 2;
       if (s >= a.stages) s -= a.stages;
+      as += 2;
+      if (as >= a.a_stages) as -= a.a_stages;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ---------------- sums of groups -> registers ----------------
     const int stream = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t from = tmem + static_cast<uint32_t>(2 * stream * kMaxCols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t from = tmem + static_cast<uint32_t>(2 * stream * a.slot_cols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int chunks = a.cols / 16;
     uint64_t acc[kMaxCols / 2];  // pairs of neighbouring tokens, for the packed multiply-add
 #pragma unroll
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t s = __float_as_uint(scale[(ss * UNITS + u) * kQuantRows]);
       const uint64_t ss2 = pair_u32(s, s);
-      const uint32_t at = from + turn * kMaxCols;
+      const uint32_t at = from + turn * static_cast<uint32_t>(a.slot_cols);
       uint32_t v[2][16];
       ld_16(at, v[0]);
 #pragma unroll
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kTmemCols)));
   }
 }
 
@@ -749,6 +751,10 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   TcQuantArgs a{};
   a.q = q;
   a.cols = p.cols;
+  // what the accumulators leave of TMEM holds decoded tiles: with two, decoding waits for the MMAs of few
+  // tokens (4096 x 16384, 16 rows: 24.6 us)
+  a.slot_cols = round_up(p.cols, 32);
+  a.a_stages = (kTmemCols - kSlots * a.slot_cols) / kACols / 2 * 2;
   a.parts = parts;
   a.part_rows = static_cast<int>(q.rows);
   a.stages = p.stages;
