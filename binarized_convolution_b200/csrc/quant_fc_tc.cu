@@ -22,8 +22,10 @@
 // is taken out while the next one is formed.  What the one MMA-issuing thread does between two
 // tiles is on the critical path, so it has few barriers: one per tile for everything that the MMAs
 // read (tokens, scales, codes) and one for its release, and two per accumulator slot.
-// Where there are few tiles, a cluster of CTAs shares a tile's input channels and adds up its parts over
-// distributed shared memory in rank order.
+// A CTA walks over its tiles without a pause: tokens and codes of the next one are on their way and decoded
+// while the sums of the last are written (a CTA per tile spent 8 us a tile outside its loop over
+// the input channels: 44 of 140 us for 2000 x 4096 x 8192).  Where there are few tiles, a cluster of CTAs
+// shares a tile's input channels and adds up its parts over distributed shared memory in rank order.
 //
 // Bound by HBM (the codes) for few tokens and by the tensor cores (4 N cycles per 128 input channels)
 // for many; groups of 32 and 64 are bound by taking out their sums.
@@ -67,7 +69,7 @@ struct __align__(16) Bars {
   uint32_t abort_flag;
 };
 
-// shared memory: [tokens][codes, zeros][scales] in whole KB, the barriers behind them
+// shared memory: [tokens][exchange][codes, zeros][scales] in whole KB, the barriers behind them
 constexpr int kRingBytes = (kSmemBytes - static_cast<int>(sizeof(Bars))) / 1024 * 1024;
 
 struct TcQuantArgs {
@@ -78,6 +80,8 @@ struct TcQuantArgs {
   int parts;       // bf16 parts of the input (3 for fp32)
   int part_rows;   // rows between the parts in the tensor map
   int stages;      // tiles of tokens in flight
+  int tiles;       // of 128 channels x HALVES * cols tokens
+  int exchange;    // bytes for the sums of the second stream (one half of tokens, CTAs of several tiles)
   int units;       // groups per 128 input channels (1 for groups of 128 and more)
   int splits;      // CTAs of a cluster sharing a tile
   int out_dtype;
@@ -244,14 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // a cluster's CTAs share the input channels of one tile; otherwise tiles cta, cta + ctas, ...
   const int split = static_cast<int>(blockIdx.x) % a.splits;
-  const int tile = blockIdx.x / a.splits;
+  const int tile0 = blockIdx.x / a.splits, tile_step = gridDim.x / a.splits;
   const int row_tiles = a.q.no_pad / kQuantRows;
-  const int rt = tile % row_tiles;
-  const int64_t token0 = static_cast<int64_t>(tile / row_tiles) * (HALVES * a.cols);
   const int per = (a.q.k_tiles + a.splits - 1) / a.splits;
   const int kt0 = min(split * per, a.q.k_tiles);
-  const int n = min(kt0 + per, a.q.k_tiles) - kt0;  // tiles of this CTA
+  const int n = min(kt0 + per, a.q.k_tiles) - kt0;  // steps (of 128 input channels) of a tile
+  const int my_tiles = tile0 < a.tiles ? (a.tiles - tile0 + tile_step - 1) / tile_step : 0;
+  const int steps = my_tiles * n;
   const int piece_bytes = a.cols * kQuantK * 2;     // [64-channel block][token][128 bytes]
   const int pieces = HALVES * a.parts;              // of a tile: halves of the tokens or parts of the input
   const int stage_b = pieces * piece_bytes;
@@ -289,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = B->tmem_base;
   const uint32_t tmem_a = tmem + static_cast<uint32_t>(kSlots * a.slot_cols);
   const int groups = (a.q.k + a.q.group - 1) / a.q.group;
-  // first of the tile's channels in a [groups][no_pad] array (behind the last group the inputs are 0)
-  auto group_at = [&](int i, int u) {
+  // first of a tile's channels in a [groups][no_pad] array (behind the last group the inputs are 0)
+  auto group_at = [&](int rt, int i, int u) {
     const int g = min(((kt0 + i) * kQuantK + u * kGroup) / a.q.group, groups - 1);
     return static_cast<int64_t>(g) * a.q.no_pad + rt * kQuantRows;
   };
@@ -305,25 +310,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, ss = 0, issued = 0;
         uint32_t phase = 1;
         const uint32_t bytes = static_cast<uint32_t>(stage_b + kScaleBytes);
-        for (int i = 0; i < n; ++i) {
-          if (!wait(done + 8 * s, phase, B, err)) break;
-          mbar_expect_tx(&B->ready[s], bytes);
-          uint8_t* to = ring_b + s * stage_b;
-          int at = static_cast<int>(token0);
-          const int c = (kt0 + i) * kQuantK;
-          for (int p = 0; p < pieces; ++p, to += piece_bytes) {
-            tma_load_2d(to, &tmB, &B->ready[s], c, at);
-            tma_load_2d(to + a.cols * 128, &tmB, &B->ready[s], c + 64, at);
-            at += HALVES == 2 ? a.cols : a.part_rows;
-          }
-          for (int u = 0; u < UNITS; ++u)
-            bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group_at(i, u), kQuantRows * 4,
-                      &B->ready[s]);
-          ++issued;
-          if (++ss == scale_stages) ss = 0;
-          if (++s == a.stages) {
-            s = 0;
-            phase ^= 1u;
+        bool ok = true;
+        for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
+          const int rt = tile % row_tiles, token0 = tile / row_tiles * (HALVES * a.cols);
+          for (int i = 0; i < n; ++i) {
+            if (!(ok = wait(done + 8 * s, phase, B, err))) break;
+            mbar_expect_tx(&B->ready[s], bytes);
+            uint8_t* to = ring_b + s * stage_b;
+            int at = token0;
+            const int c = (kt0 + i) * kQuantK;
+            for (int p = 0; p < pieces; ++p, to += piece_bytes) {
+              tma_load_2d(to, &tmB, &B->ready[s], c, at);
+              tma_load_2d(to + a.cols * 128, &tmB, &B->ready[s], c + 64, at);
+              at += HALVES == 2 ? a.cols : a.part_rows;
+            }
+            for (int u = 0; u < UNITS; ++u)
+              bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group_at(rt, i, u), kQuantRows * 4,
+                        &B->ready[s]);
+            ++issued;
+            if (++ss == scale_stages) ss = 0;
+            if (++s == a.stages) {
+              s = 0;
+              phase ^= 1u;
+            }
           }
         }
         if (*reinterpret_cast<volatile uint32_t*>(&B->abort_flag)) drain(B->ready, a.stages, issued);
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t turn = 0, empty_ph = 1, stream = 0;
         int s = 0, as = 0;
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
+        for (int i = 0; i < steps && ok; ++i) {
           if (!(ok = wait(ready + 8 * s, ready_ph, B, err))) break;
           const uint32_t a_tmem = tmem_a + static_cast<uint32_t>(as * kACols);
           if (++as == a.a_stages) as = 0;
@@ -394,40 +403,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       if (elect_one()) {
         // ---------------- codes and zeros ----------------
-        const uint8_t* from =
-            reinterpret_cast<const uint8_t*>(a.q.codes) + (static_cast<int64_t>(rt) * a.q.k_tiles + kt0) * kQuantTileBytes;
         int s = 0, issued = 0;
         uint32_t phase = 1;
-        for (int i = 0; i < n; ++i, from += kQuantTileBytes) {
-          if (!wait(empty_w + 8 * s, phase, B, err)) {
-            drain(B->full_w, kWStages, issued);
-            break;
-          }
-          ++issued;
-          uint8_t* to = ring_w + s * stage_w;
-          mbar_expect_tx(&B->full_w[s], static_cast<uint32_t>(stage_w));
-          bulk_load(to, from, kQuantTileBytes, &B->full_w[s]);
-          if (a.q.zero)
-            for (int u = 0; u < UNITS; ++u)
-              bulk_load(to + kQuantTileBytes + u * kQuantRows, a.q.zero + group_at(i, u), kQuantRows, &B->full_w[s]);
-          if (++s == kWStages) {
-            s = 0;
-            phase ^= 1u;
+        bool ok = true;
+        for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
+          const int rt = tile % row_tiles;
+          const uint8_t* from = reinterpret_cast<const uint8_t*>(a.q.codes) +
+                                (static_cast<int64_t>(rt) * a.q.k_tiles + kt0) * kQuantTileBytes;
+          for (int i = 0; i < n; ++i, from += kQuantTileBytes) {
+            if (!(ok = wait(empty_w + 8 * s, phase, B, err))) break;
+            ++issued;
+            uint8_t* to = ring_w + s * stage_w;
+            mbar_expect_tx(&B->full_w[s], static_cast<uint32_t>(stage_w));
+            bulk_load(to, from, kQuantTileBytes, &B->full_w[s]);
+            if (a.q.zero)
+              for (int u = 0; u < UNITS; ++u)
+                bulk_load(to + kQuantTileBytes + u * kQuantRows, a.q.zero + group_at(rt, i, u), kQuantRows, &B->full_w[s]);
+            if (++s == kWStages) {
+              s = 0;
+              phase ^= 1u;
+            }
           }
         }
+        if (!ok) drain(B->full_w, kWStages, issued);
       }
     }
     __syncwarp();
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    // ---------------- codes -> operands: tiles odd, odd + 2, ... ----------------
+    // ---------------- codes -> operands: steps odd, odd + 2, ... ----------------
     const int odd = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int ws = odd % kWStages, as = odd;
     uint32_t wph = 0;
-    int s = odd % a.stages, ds = odd % a.stages;  // of tile i and of tile i - a_stages, whose place it takes
+    int s = odd % a.stages, ds = odd % a.stages;  // of step i and of step i - a_stages, whose place it takes
     uint32_t dph = 0;
-    for (int i = odd; i < n; i += 2) {
+    for (int i = odd; i < steps; i += 2) {
       if (!wait_warp(full_w + 8 * ws, wph, B, err)) break;
       const uint8_t* from = ring_w + ws * stage_w + row * 16;
       uint32_t w[4][4];
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < 4; ++p)
               v[c * 16 + t * 4 + p] =
                   decode<HALF>((w[t][2 * two + c] >> (4 * p)) & 0x000f000fu, zz[2 * two + c]);
-        if (two == 0) {  // the place is free when the MMAs of tile i - a_stages are done
+        if (two == 0) {  // the place is free when the MMAs of step i - a_stages are done
           if (i >= a.a_stages) {
             ok = wait_warp(done + 8 * ds, dph, B, err);
             ds += 2;
@@ -493,93 +504,142 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int stream = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t from = tmem + static_cast<uint32_t>(2 * stream * a.slot_cols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int chunks = a.cols / 16;
-    uint64_t acc[kMaxCols / 2];  // pairs of neighbouring tokens, for the packed multiply-add
-#pragma unroll
-    for (int j = 0; j < kMaxCols / 2; ++j) acc[j] = 0;
     bool ok = true;
     uint32_t turn = 0, phase = 0;
     const float* scale = reinterpret_cast<const float*>(ring_s) + row;
-    int ss = 0, u = 0;  // the unit's scales
+    int ss = 0, u = 0;  // of this stream's next unit
     if (HALVES == 1 && stream) {
       if (UNITS == 1) ss = 1;
       else u = 1;
     }
-    const int total = HALVES == 2 ? n * UNITS : (n * UNITS + 1 - stream) / 2;
-    for (int i = 0; i < total; ++i) {
-      const uint32_t slot = 2u * stream + turn;
-      if (!(ok = wait_warp(full_d + 8 * slot, phase, B, err))) break;
-      tc_fence_after();
-      const uint32_t s = __float_as_uint(scale[(ss * UNITS + u) * kQuantRows]);
-      const uint64_t ss2 = pair_u32(s, s);
-      const uint32_t at = from + turn * static_cast<uint32_t>(a.slot_cols);
-      uint32_t v[2][16];
-      ld_16(at, v[0]);
+    // units of a tile; with one half, this stream's are those of its parity, counted through all tiles
+    const int units = n * UNITS;
+    int unit = HALVES == 2 ? 0 : stream;  // this stream's next unit, relative to the tile
+    float* const xchg = reinterpret_cast<float*>(a.exchange ? smem + kRingBytes - scale_stages * kScaleBytes -
+                                                                   kWStages * stage_w - a.exchange
+                                                             : ring_b);
+    for (int tile = tile0; tile < a.tiles; tile += tile_step) {
+      const int rt = tile % row_tiles;
+      const int64_t token0 = static_cast<int64_t>(tile / row_tiles) * (HALVES * a.cols);
+      uint64_t acc[kMaxCols / 2];  // pairs of neighbouring tokens, for the packed multiply-add
 #pragma unroll
-      for (int c = 0; c < kMaxCols / 16; ++c)
-        if (c < chunks) {
-          ld_wait(v[c & 1]);
-          if (c + 1 < kMaxCols / 16 && c + 1 < chunks) {
-            ld_16(at + static_cast<uint32_t>((c + 1) * 16), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (elect_one()) arrive(empty_d + 8 * slot);
+      for (int j = 0; j < kMaxCols / 2; ++j) acc[j] = 0;
+      for (; unit < units && ok; unit += HALVES == 2 ? 1 : 2) {
+        const uint32_t slot = 2u * stream + turn;
+        if (!(ok = wait_warp(full_d + 8 * slot, phase, B, err))) break;
+        tc_fence_after();
+        const uint32_t sc = __float_as_uint(scale[(ss * UNITS + u) * kQuantRows]);
+        const uint64_t sc2 = pair_u32(sc, sc);
+        const uint32_t at = from + turn * static_cast<uint32_t>(a.slot_cols);
+        uint32_t v[2][16];
+        ld_16(at, v[0]);
+#pragma unroll
+        for (int c = 0; c < kMaxCols / 16; ++c)
+          if (c < chunks) {
+            ld_wait(v[c & 1]);
+            if (c + 1 < kMaxCols / 16 && c + 1 < chunks) {
+              ld_16(at + static_cast<uint32_t>((c + 1) * 16), v[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (elect_one()) arrive(empty_d + 8 * slot);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[c * 8 + j] = fma_f32x2(sc2, pair_u32(v[c & 1][2 * j], v[c & 1][2 * j + 1]), acc[c * 8 + j]);
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[c * 8 + j] = fma_f32x2(ss2, pair_u32(v[c & 1][2 * j], v[c & 1][2 * j + 1]), acc[c * 8 + j]);
+        turn ^= 1u;
+        if (turn == 0) phase ^= 1u;
+        u += HALVES == 2 ? 1 : 2;
+        while (u >= UNITS) {
+          u -= UNITS;
+          if (++ss == scale_stages) ss = 0;
         }
-      turn ^= 1u;
-      if (turn == 0) phase ^= 1u;
-      u += HALVES == 2 ? 1 : 2;
-      while (u >= UNITS) {
-        u -= UNITS;
-        if (++ss == scale_stages) ss = 0;
       }
-    }
-    // this CTA's sums as [token][channel] over the token ring (all MMAs that read it are done), so that a
-    // warp writes 128 channels of a token at a time
-    named_barrier(256);
-    float* const mine = reinterpret_cast<float*>(ring_b) + (HALVES == 2 ? stream * a.cols * kQuantRows : 0) + row;
-    if (HALVES == 2 || stream == 0)
-#pragma unroll
-      for (int c = 0; c < kMaxCols / 16; ++c)
-        if (c < chunks) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] = half_of(acc[c * 8 + j / 2], j & 1);
-        }
-    if (HALVES == 1) {  // the other half of the units
-      named_barrier(256);
-      if (stream == 1)
+      // (having given up, this stream still meets the other one at every barrier)
+      unit -= units;
+      // one half: the second stream's sums go through shared memory, [token][channel], to the first's threads
+      const bool both = HALVES == 1 && a.splits == 1;
+      if (both && !a.exchange) named_barrier(256);  // (over the token ring: all MMAs that read it are done)
+      if (both && stream == 1) {
 #pragma unroll
         for (int c = 0; c < kMaxCols / 16; ++c)
           if (c < chunks) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] += half_of(acc[c * 8 + j / 2], j & 1);
+            for (int j = 0; j < 16; ++j) xchg[(c * 16 + j) * kQuantRows + row] = half_of(acc[c * 8 + j / 2], j & 1);
           }
-    }
-    if (a.splits > 1)
-      asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else
-      named_barrier(256);
-    if (ok && !*reinterpret_cast<volatile uint32_t*>(&B->abort_flag)) {
-      // tokens split, split + splits, ... of the tile, the warps taking turns; four channels a lane
-      const int w = warp - 12, c0 = rt * kQuantRows + lane * 4;
-      float bias[4] = {0.f, 0.f, 0.f, 0.f};
-      if (a.q.bias)
+      }
+      if (both) named_barrier(256);
+      if (ok && a.splits == 1 && (HALVES == 2 || stream == 0)) {
+        // a lane's channel, token by token: a warp writes 32 neighbouring channels
+        const int chan = rt * kQuantRows + row;
+        const int64_t first = token0 + (HALVES == 2 ? stream * a.cols : 0);
+        const int count = static_cast<int>(min(static_cast<int64_t>(a.cols), a.q.rows - first));
+        if (chan < a.q.no) {
+          const float bias = a.q.bias ? __ldg(a.q.bias + chan) : 0.f;
+          auto write = [&](auto* out) {
+            using TOut = std::remove_pointer_t<decltype(out)>;
+            out += first * a.q.out_stride + chan;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c0 + i < a.q.no) bias[i] = __ldg(a.q.bias + c0 + i);
+            for (int c = 0; c < kMaxCols / 16; ++c)
+              if (c * 16 < count) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  float y = half_of(acc[c * 8 + j / 2], j & 1) + bias;
+                  if (HALVES == 1) y += xchg[(c * 16 + j) * kQuantRows + row];
+                  if (a.q.relu) y = y < 0.f ? 0.f : y;
+                  if (c * 16 + j < count) *out = from_f32<TOut>(y);
+                  out += a.q.out_stride;
+                }
+              }
+          };
+          if (a.out_dtype == BCONV_DTYPE_F32) write(static_cast<float*>(a.q.out));
+          else if (a.out_dtype == BCONV_DTYPE_BF16) write(static_cast<__nv_bfloat16*>(a.q.out));
+          else write(static_cast<__half*>(a.q.out));
+        }
+      }
+      if (both) named_barrier(256);  // (before the sums of the next tile)
+      if (a.splits > 1) {
+        // one tile: this CTA's sums as [token][channel] over the token ring (all MMAs that read it are done), so
+        // that a warp adds up and writes 128 channels of a token at a time
+        named_barrier(256);
+        float* const mine = reinterpret_cast<float*>(ring_b) + (HALVES == 2 ? stream * a.cols * kQuantRows : 0) + row;
+        if (HALVES == 2 || stream == 0)
+#pragma unroll
+          for (int c = 0; c < kMaxCols / 16; ++c)
+            if (c < chunks) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] = half_of(acc[c * 8 + j / 2], j & 1);
+            }
+        if (HALVES == 1) {  // the other half of the units
+          named_barrier(256);
+          if (stream == 1)
+#pragma unroll
+            for (int c = 0; c < kMaxCols / 16; ++c)
+              if (c < chunks) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) mine[(c * 16 + j) * kQuantRows] += half_of(acc[c * 8 + j / 2], j & 1);
+              }
+        }
+      }
+    }
+    if (a.splits > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (ok && !*reinterpret_cast<volatile uint32_t*>(&B->abort_flag)) {
+        // tokens split, split + splits, ... of the tile, the warps taking turns; four channels a lane
+        const int rt = tile0 % row_tiles;
+        const int64_t token0 = static_cast<int64_t>(tile0 / row_tiles) * (HALVES * a.cols);
+        const int w = warp - 12, c0 = rt * kQuantRows + lane * 4;
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+        if (a.q.bias)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c0 + i < a.q.no) bias[i] = __ldg(a.q.bias + c0 + i);
 #pragma unroll 1
-      for (int j = split + w * a.splits; j < HALVES * a.cols; j += 8 * a.splits) {
-        const int64_t token = token0 + j;
-        if (token >= a.q.rows) break;
-        float4 v;
-        if (a.splits == 1) {
-          v = reinterpret_cast<const float4*>(ring_b)[j * 32 + lane];
-        } else {
-          v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float4 p[kMaxSplit];
+        for (int j = split + w * a.splits; j < HALVES * a.cols; j += 8 * a.splits) {
+          const int64_t token = token0 + j;
+          if (token >= a.q.rows) break;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f), p[kMaxSplit];
 #pragma unroll
           for (int i = 0; i < kMaxSplit; ++i)
             if (i < a.splits) {
@@ -594,15 +654,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i < a.splits) {
               v.x += p[i].x; v.y += p[i].y; v.z += p[i].z; v.w += p[i].w;
             }
-        }
-        float y[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
-        if (a.q.relu)
+          float y[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
+          if (a.q.relu)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
-        const int64_t at = token * a.q.out_stride + c0;
-        if (a.out_dtype == BCONV_DTYPE_F32) put4(static_cast<float*>(a.q.out) + at, y, a.q.no - c0);
-        else if (a.out_dtype == BCONV_DTYPE_BF16) put4(static_cast<__nv_bfloat16*>(a.q.out) + at, y, a.q.no - c0);
-        else put4(static_cast<__half*>(a.q.out) + at, y, a.q.no - c0);
+            for (int i = 0; i < 4; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
+          const int64_t at = token * a.q.out_stride + c0;
+          if (a.out_dtype == BCONV_DTYPE_F32) put4(static_cast<float*>(a.q.out) + at, y, a.q.no - c0);
+          else if (a.out_dtype == BCONV_DTYPE_BF16) put4(static_cast<__nv_bfloat16*>(a.q.out) + at, y, a.q.no - c0);
+          else put4(static_cast<__half*>(a.q.out) + at, y, a.q.no - c0);
+        }
       }
     }
   }
@@ -648,7 +708,7 @@ __global__ void quant_fc_stage_kernel(const T* __restrict__ in, int64_t stride, 
 }
 
 struct Plan {
-  int halves, cols, stages, splits;
+  int halves, cols, stages, splits, exchange;
   int64_t tiles;
 };
 
@@ -671,16 +731,17 @@ Plan plan_for(const QuantFcArgs& q, int parts) {
       while (splits < kMaxSplit && tiles * splits * 2 <= sms && q.k_tiles >= splits * 4) splits *= 2;
       const double per = std::max(4.0 * halves * cols * parts, static_cast<double>(kFloor));
       const double cost = static_cast<double>(ceil_div(tiles * splits, sms)) *
-                          (per * static_cast<double>(ceil_div(q.k_tiles, splits)) + 3000.0 + 8.0 * halves * cols);
+                          (per * static_cast<double>(ceil_div(q.k_tiles, splits)) + 1000.0 + 8.0 * halves * cols);
       if (cost < best_cost) {
         best_cost = cost;
-        best = {halves, cols, 0, splits, tiles};
+        best = {halves, cols, 0, splits, 0, tiles};
       }
     }
   }
   const int units = q.group >= kQuantK ? 1 : kQuantK / q.group;
   const int scale = units * kQuantRows * 4;
-  const int left = kRingBytes - kWStages * w_stage_bytes(units, q.zero) - kScaleSlack * scale;
+  best.exchange = best.halves == 1 && best.tiles > sms ? best.cols * kQuantRows * 4 : 0;
+  const int left = kRingBytes - kWStages * w_stage_bytes(units, q.zero) - kScaleSlack * scale - best.exchange;
   best.stages = std::min(kMaxStages, left / (best.halves * parts * best.cols * kQuantK * 2 + scale));
   return best;
 }
@@ -703,7 +764,7 @@ cudaError_t launch(const CUtensorMap& map, const TcQuantArgs& a, int64_t tiles, 
   cudaError_t e = allow_smem<quant_fc_tc_kernel<HALVES, HALF, UNITS>>(kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.splits > 1 ? tiles * a.splits : std::min<int64_t>(tiles, current_sm_count())));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
@@ -751,17 +812,20 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   TcQuantArgs a{};
   a.q = q;
   a.cols = p.cols;
-  // what the accumulators leave of TMEM holds decoded tiles: with two, decoding waits for the MMAs of few
-  // tokens (4096 x 16384, 16 rows: 24.6 us)
+  // What the accumulators leave of TMEM holds decoded tiles, but no more of them than tokens: step i arrives on
+  // the barrier of step i - stages, whose phase must be over.
   a.slot_cols = round_up(p.cols, 32);
-  a.a_stages = (kTmemCols - kSlots * a.slot_cols) / kACols / 2 * 2;
+  a.a_stages = std::min((kTmemCols - kSlots * a.slot_cols) / kACols, p.stages) / 2 * 2;
   a.parts = parts;
   a.part_rows = static_cast<int>(q.rows);
   a.stages = p.stages;
+  a.tiles = static_cast<int>(p.tiles);
+  a.exchange = p.exchange;
   a.units = q.group >= kQuantK ? 1 : kQuantK / q.group;
   a.splits = p.splits;
   a.out_dtype = out_dtype;
   a.staged = staged;
+  if (a.stages < 2 || a.a_stages < 2 || a.cols > kMaxCols) return cudaErrorInvalidValue;
   auto enc = encoder();
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap map;
