@@ -79,6 +79,33 @@ __device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8]
   }
 }
 
+// The same in a loop that skips a thread's vectors behind the row (`absent`): filling them with zeros, load by load,
+// was a sixth of the backward's instructions.
+template <bool VEC>
+__device__ __forceinline__ bool absent(int j, int C) {
+  return VEC && channel<true>(j, 0, blockDim.x) >= C;
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void get8(const T* row, int j, int C, float (&v)[8]) {
+  if (VEC) {
+    Raw8<T> w;
+    w.load(row + channel<true>(j, 0, blockDim.x));
+    w.unpack(v);
+  } else {
+    load8<false>(row, j, C, v);
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void put8(T* row, int j, int C, const float (&v)[8]) {
+  if (VEC) {
+    Raw8<T> w;
+    w.pack(v);
+    w.store(row + channel<true>(j, 0, blockDim.x));
+  } else {
+    store8<false>(row, j, C, v);
+  }
+}
+
 // Sums of N values over the CTA's first t threads (which meet at barrier 1), the same in every thread and in
 // a fixed order.  `buf` is one of two areas of 32 * N floats used in turn, so one barrier per call is enough.
 template <int N>
@@ -536,8 +563,9 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
   if (a.pre)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (absent<VEC>(j, C)) continue;
       float w[8];
-      load8<VEC>(a.pre, j, C, w);
+      get8<VEC>(a.pre, j, C, w);
       pre.put(j, w);
     }
   if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
@@ -553,9 +581,10 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
     float r[NV][8], b[NV][8], q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load8<VEC>(r_row, j, C, r[j]);
+      if (absent<VEC>(j, C)) continue;
+      get8<VEC>(r_row, j, C, r[j]);
       if (a.block) {
-        load8<VEC>(b_row, j, C, b[j]);
+        get8<VEC>(b_row, j, C, b[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[0] = fmaf(b[j][e], b[j][e], q[0]);
       }
@@ -573,6 +602,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
       const float bs = a.post ? rsqrtf(fmaf(q[0], inv, a.eps)) : 1.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
         float w[8];
         gate_post.get(j, w);
 #pragma unroll
@@ -581,22 +611,26 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
     }
     if (a.residual_out)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store8<VEC>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+      for (int j = 0; j < NV; ++j)
+        if (!absent<VEC>(j, C)) put8<VEC>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
     if (a.normed) {
       float t[1] = {0.f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[0] = fmaf(r[j][e], r[j][e], t[0]);
+      }
       block_sums(t, sums[1]);
       const float rs = rsqrtf(fmaf(t[0], inv, a.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
         float w[8];
         pre.get(j, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[j][e] = r[j][e] * rs * w[e];
-        store8<VEC>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
+        put8<VEC>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
       }
     }
     if (a.post && !a.normed) __syncthreads();  // (otherwise there are two barriers a row, and the areas alternate)
@@ -630,8 +664,9 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   if (a.pre)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (absent<VEC>(j, C)) continue;
       float w[8];
-      load8<VEC>(a.pre, j, C, w);
+      get8<VEC>(a.pre, j, C, w);
       pre.put(j, w);
     }
   if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
@@ -648,23 +683,24 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   auto flush = [&]() {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (absent<VEC>(j, C)) continue;
       float w[8];
       if (gate_to) {
-        if (a.post) load8<VEC>(a.post, j, C, w);
+        if (a.post) get8<VEC>(a.post, j, C, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = a.post ? w[e] * sum[j][e] : sum[j][e];
-        store8<VEC>(gate_to, j, C, w);
+        put8<VEC>(gate_to, j, C, w);
       }
       if (a.sum_post) {
         float t[8];
-        if (g_row) load8<VEC>(g_row, j, C, w);
-        if (flushed) load8<VEC>(a.sum_post + cta * C, j, C, t);
+        if (g_row) get8<VEC>(g_row, j, C, w);
+        if (flushed) get8<VEC>(a.sum_post + cta * C, j, C, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float add = g_row ? w[e] * sum[j][e] : sum[j][e];
           t[e] = flushed ? t[e] + add : add;
         }
-        store8<VEC>(a.sum_post + cta * C, j, C, t);
+        put8<VEC>(a.sum_post + cta * C, j, C, t);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[j][e] = 0.f;
@@ -692,10 +728,11 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     float t[3] = {0.f, 0.f, 0.f};  // r'^2, u r', b^2
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (absent<VEC>(j, C)) continue;
       if (a.d_normed) {
         float r[8], dn[8], w[8];
-        load8<VEC>(r_row, j, C, r);
-        load8<VEC>(dn_row, j, C, dn);
+        get8<VEC>(r_row, j, C, r);
+        get8<VEC>(dn_row, j, C, dn);
         pre.get(j, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -705,7 +742,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       }
       if (a.post) {
         float b[8];
-        load8<VEC>(b_row, j, C, b);
+        get8<VEC>(b_row, j, C, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[2] = fmaf(b[e], b[e], t[2]);
       }
@@ -722,17 +759,18 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     float c[1] = {0.f}, v[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (absent<VEC>(j, C)) continue;
       float dr[8], w[8];
       if (a.d_out) {
-        load8<VEC>(do_row, j, C, dr);
+        get8<VEC>(do_row, j, C, dr);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dr[e] = 0.f;
       }
       if (a.d_normed) {
         float r[8], dn[8];
-        load8<VEC>(r_row, j, C, r);
-        load8<VEC>(dn_row, j, C, dn);
+        get8<VEC>(r_row, j, C, r);
+        get8<VEC>(dn_row, j, C, dn);
         pre.get(j, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -740,10 +778,10 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
           apre[j][e] = fmaf(dn[e], r[e] * rs, apre[j][e]);
         }
       }
-      if (a.d_residual) store8<VEC>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
+      if (a.d_residual) put8<VEC>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
       if (a.block) {
         float b[8];
-        load8<VEC>(b_row, j, C, b);
+        get8<VEC>(b_row, j, C, b);
         gate_post.get(j, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -762,11 +800,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       if (a.d_block)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+          if (absent<VEC>(j, C)) continue;
           float b[8];
-          load8<VEC>(b_row, j, C, b);
+          get8<VEC>(b_row, j, C, b);
 #pragma unroll
           for (int e = 0; e < 8; ++e) b[e] = bs * (v[j][e] - b[e] * mb);
-          store8<VEC>(static_cast<T*>(a.d_block) + row * C, j, C, b);
+          put8<VEC>(static_cast<T*>(a.d_block) + row * C, j, C, b);
         }
     }
     if (!a.block || !a.post) __syncthreads();  // with both reductions, their areas alternate
@@ -778,7 +817,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   flush();
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (a.sum_pre) store8<VEC>(a.sum_pre + cta * C, j, C, apre[j]);
+    if (a.sum_pre && !absent<VEC>(j, C)) put8<VEC>(a.sum_pre + cta * C, j, C, apre[j]);
 }
 
 struct SumArgs {
@@ -824,6 +863,7 @@ __global__ void block_norm_sum_kernel(const SumArgs a) {
   float s = 0.f;
   if (c < a.C) {
     if (extra && threadIdx.y == 0) s = extra[c];
+#pragma unroll 8
     for (int64_t i = threadIdx.y; i < n; i += kSumRows) s += from[i * step + c];
   }
   part[threadIdx.y][threadIdx.x] = s;
