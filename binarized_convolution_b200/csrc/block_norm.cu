@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
 // Rows need no alignment: a copy takes the 16-byte pieces that hold the row, which then lies at
 // the same offset from a 16-byte boundary as in memory.
 
-constexpr int kRingLow = 1024, kRingHigh = 8192;  // widths served
+constexpr int kRingLow = 256, kRingHigh = 8192;  // widths served
 constexpr int kRingNv = 2;                       // 8-channel vectors of a thread
 constexpr int kRingBytes = 216 * 1024;           // of an SM
 constexpr int kMaxRing = 4;
@@ -1086,7 +1086,10 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   const bool vec = d->width % 8 == 0 && all_aligned16({residual_out, block, gate, d_residual_out, d_normed, post_weight,
                                                        pre_weight, d_residual, d_block, d_gate, workspace});
   const Shape sh = shape_for(d->width, 4);
-  const bool ring = many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 4);
+  // Unaligned fp32 rows up to 4096 channels are left to the plain kernel, which keeps all its sums in registers (8000 x
+  // 2001: 173 us against 322; 16-bit rows 247 against 238, 8000 x 4099 fp32 1023 against 624).
+  const bool ring = many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 4) &&
+                    (vec || d->dtype != BCONV_DTYPE_F32 || d->width > 4096);
   e = with_dtype(d->dtype, [&](auto t) {
     using T = decltype(t);
     if (ring) return vec ? launch_bwd_ring<T, true>(a, ctas, stream) : launch_bwd_ring<T, false>(a, ctas, stream);

@@ -8,7 +8,8 @@
 // and exact in bf16 and fp16, so the tensor cores sum exact products of the input (kind::f16 with
 // fp32 accumulators) and every group's sum is scaled and added in fp32 registers; no weight is
 // ever rounded.  fp32 inputs come as three bf16 parts whose sum they are (see stage_kernel), each
-// multiplied by the same codes.
+// multiplied by the same codes: one after the other into the same sums, or, for up to 32 rows, as three times as many
+// tokens (9 rows of 25088 channels: a third of the MMAs).
 //
 // The codes become operands in TMEM, not in shared memory: eight warps read a tile's packed codes (8
 // KB per 128 x 128, one bulk copy) and write them with tcgen05.st as the MMA's A operand, one
@@ -77,7 +78,8 @@ struct TcQuantArgs {
   int cols;        // tokens of an MMA (a multiple of 16, at most kMaxCols)
   int slot_cols;   // TMEM columns between the accumulators
   int a_stages;    // decoded tiles in TMEM (even: the decoding warpgroups take turns)
-  int parts;       // bf16 parts of the input (3 for fp32)
+  int parts;       // bf16 parts of the input (3 for fp32), multiplied one after the other
+  int fold;        // or 3 parts as rows of their own, whose sums are added up at the end
   int part_rows;   // rows between the parts in the tensor map
   int stages;      // tiles of tokens in flight
   int tiles;       // of 128 channels x HALVES * cols tokens
@@ -257,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = min(kt0 + per, a.q.k_tiles) - kt0;  // steps (of 128 input channels) of a tile
   const int my_tiles = tile0 < a.tiles ? (a.tiles - tile0 + tile_step - 1) / tile_step : 0;
   const int steps = my_tiles * n;
+  const bool joined = a.splits > 1 || a.fold > 1;  // sums that meet in shared memory (one tile a CTA)
   const int piece_bytes = a.cols * kQuantK * 2;     // [64-channel block][token][128 bytes]
   const int pieces = HALVES * a.parts;              // of a tile: halves of the tokens or parts of the input
   const int stage_b = pieces * piece_bytes;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (having given up, this stream still meets the other one at every barrier)
       unit -= units;
       // one half: the second stream's sums go through shared memory, [token][channel], to the first's threads
-      const bool both = HALVES == 1 && a.splits == 1;
+      const bool both = HALVES == 1 && !joined;
       if (both && !a.exchange) named_barrier(256);  // (over the token ring: all MMAs that read it are done)
       if (both && stream == 1) {
 #pragma unroll
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
       if (both) named_barrier(256);
-      if (ok && a.splits == 1 && (HALVES == 2 || stream == 0)) {
+      if (ok && !joined && (HALVES == 2 || stream == 0)) {
         // a lane's channel, token by token: a warp writes 32 neighbouring channels
         const int chan = rt * kQuantRows + row;
         const int64_t first = token0 + (HALVES == 2 ? stream * a.cols : 0);
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (both) named_barrier(256);  // (before the sums of the next tile)
-      if (a.splits > 1) {
+      if (joined) {
         // one tile: this CTA's sums as [token][channel] over the token ring (all MMAs that read it are done), so
         // that a warp adds up and writes 128 channels of a token at a time
         named_barrier(256);
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (a.splits > 1) {
+    if (joined) {
       asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
       if (ok && !*reinterpret_cast<volatile uint32_t*>(&B->abort_flag)) {
         // tokens split, split + splits, ... of the tile, the warps taking turns; four channels a lane
@@ -639,21 +642,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = split + w * a.splits; j < HALVES * a.cols; j += 8 * a.splits) {
           const int64_t token = token0 + j;
           if (token >= a.q.rows) break;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f), p[kMaxSplit];
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int f = a.fold - 1; f >= 0; --f) {  // (the smallest part first)
+            const uint32_t line = static_cast<uint32_t>((j + f * static_cast<int>(a.q.rows)) * 32 + lane) * 16u;
+            float4 p[kMaxSplit];
 #pragma unroll
-          for (int i = 0; i < kMaxSplit; ++i)
-            if (i < a.splits) {
-              const uint32_t at = mapa(ring_b, static_cast<uint32_t>(i)) + static_cast<uint32_t>(j * 32 + lane) * 16u;
-              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(p[i].x), "=f"(p[i].y), "=f"(p[i].z), "=f"(p[i].w)
-                           : "r"(at)
-                           : "memory");
-            }
+            for (int i = 0; i < kMaxSplit; ++i)
+              if (i < a.splits)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(p[i].x), "=f"(p[i].y), "=f"(p[i].z), "=f"(p[i].w)
+                             : "r"(mapa(ring_b, static_cast<uint32_t>(i)) + line)
+                             : "memory");
 #pragma unroll
-          for (int i = 0; i < kMaxSplit; ++i)
-            if (i < a.splits) {
-              v.x += p[i].x; v.y += p[i].y; v.z += p[i].z; v.w += p[i].w;
-            }
+            for (int i = 0; i < kMaxSplit; ++i)
+              if (i < a.splits) {
+                v.x += p[i].x; v.y += p[i].y; v.z += p[i].z; v.w += p[i].w;
+              }
+          }
           float y[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
           if (a.q.relu)
 #pragma unroll
@@ -666,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (a.splits > 1) {
+  if (joined) {
     __syncwarp();
     // the taking-out warps have passed one cluster barrier already; everyone passes two
     if (warp < 12) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -712,21 +718,21 @@ struct Plan {
   int64_t tiles;
 };
 
-// Tokens per CTA and CTAs per tile.  A CTA's time for 128 input channels is about max(4 tokens,
+// Tokens per CTA and CTAs per tile, for `rows` rows of `parts` parts (one_tile: all rows in one tile).  A CTA's time for 128 input channels is about max(4 tokens,
 // kFloor) cycles: the MMAs, or reading and decoding 8 KB of codes.  Token counts that fill whole waves of
 // CTAs win over large tiles with a ragged last wave; leftover SMs share the input channels.
-Plan plan_for(const QuantFcArgs& q, int parts) {
+Plan plan_for(const QuantFcArgs& q, int64_t rows, int parts, int most_halves, bool one_tile) {
   constexpr int kFloor = 600;
   const int sms = current_sm_count();
   const int row_tiles = q.no_pad / kQuantRows;
   const int most_cols = parts == 1 ? kMaxCols : 64;  // (the parts' stages take the space)
   Plan best{};
   double best_cost = 1e300;
-  for (int halves = 1; halves <= (parts == 1 ? 2 : 1); ++halves) {
-    const int64_t least = ceil_div(q.rows, most_cols * halves);
-    for (int64_t t = least; t < least + 6; ++t) {
-      const int cols = round_up(static_cast<int>(ceil_div(ceil_div(q.rows, t), halves)), 16);
-      const int64_t tiles = ceil_div(q.rows, halves * cols) * row_tiles;
+  for (int halves = 1; halves <= most_halves; ++halves) {
+    const int64_t least = ceil_div(rows, most_cols * halves);
+    for (int64_t t = least; t < least + (one_tile ? 1 : 6); ++t) {
+      const int cols = round_up(static_cast<int>(ceil_div(ceil_div(rows, t), halves)), 16);
+      const int64_t tiles = ceil_div(rows, halves * cols) * row_tiles;
       int splits = 1;
       while (splits < kMaxSplit && tiles * splits * 2 <= sms && q.k_tiles >= splits * 4) splits *= 2;
       const double per = std::max(4.0 * halves * cols * parts, static_cast<double>(kFloor));
@@ -794,7 +800,8 @@ int64_t quant_fc_tc_workspace(int64_t rows, int k, int in_dtype) {
 cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype, void* workspace, cudaStream_t s) {
   const bool f32 = in_dtype == BCONV_DTYPE_F32, half = in_dtype == BCONV_DTYPE_F16;
   const bool staged = !quant_fc_tma_reads(q.in, q.in_stride, q.k, in_dtype);
-  const int parts = f32 ? 3 : 1;
+  const bool fold = f32 && 3 * q.rows <= kMaxCols && q.no_pad / kQuantRows <= current_sm_count();
+  const int parts = f32 && !fold ? 3 : 1;
   const int k_pad = round_up(q.k, 64);
   if (staged) {
     const int64_t n = q.rows * (k_pad / 2);
@@ -808,7 +815,7 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const Plan p = plan_for(q, parts);
+  const Plan p = fold ? plan_for(q, 3 * q.rows, 1, 1, true) : plan_for(q, q.rows, parts, parts == 1 ? 2 : 1, false);
   TcQuantArgs a{};
   a.q = q;
   a.cols = p.cols;
@@ -817,6 +824,7 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   a.slot_cols = round_up(p.cols, 32);
   a.a_stages = std::min((kTmemCols - kSlots * a.slot_cols) / kACols, p.stages) / 2 * 2;
   a.parts = parts;
+  a.fold = fold ? 3 : 1;
   a.part_rows = static_cast<int>(q.rows);
   a.stages = p.stages;
   a.tiles = static_cast<int>(p.tiles);
@@ -830,7 +838,7 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap map;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(staged ? k_pad : q.k),
-                              static_cast<cuuint64_t>(staged ? q.rows * parts : q.rows)};
+                              static_cast<cuuint64_t>(f32 ? q.rows * 3 : q.rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(staged ? k_pad : q.in_stride) * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.cols)};
   const cuuint32_t elem[2] = {1, 1};

@@ -71,6 +71,8 @@ QUANT_SHAPES = [
     (100, 4096, 300, 128), (127, 520, 136, 64), (128, 768, 256, 256), (129, 1000, 384, 128), (255, 128, 128, 32),
     (256, 2048, 512, 128), (257, 136, 264, 64), (400, 1537, 1000, 128), (700, 640, 2000, 640), (1, 25088, 64, 128),
     (5, 12544, 256, 64), (40, 25088, 130, 128), (1, 1, 1, 32), (2, 31, 3, 32), (3, 33, 5, 32),
+    # fp32: parts as rows of their own, up to 32 rows, with and without shared input channels
+    (9, 25088, 512, 128), (32, 4096, 1000, 64), (31, 640, 18900, 128), (20, 300, 19000, 32), (33, 2048, 700, 128),
     # several tiles a CTA: few tokens and many
     (40, 256, 20000, 128), (33, 160, 25000, 32), (70, 384, 30000, 64), (96, 129, 19500, 128), (17, 900, 40000, 256),
     (1500, 130, 5000, 64), (900, 256, 9000, 32), (2100, 300, 3000, 128), (4000, 64, 640, 64), (200, 1000, 20000, 128),
