@@ -216,9 +216,12 @@ class BlockNormGrad(NamedTuple):
 
 
 @functools.lru_cache(maxsize=256)
-def _norm_desc(rows, per, width, dtype, residual_scale, eps):
+def _norm_desc(device, rows, per, width, dtype, residual_scale, eps):
+    """The C descriptor (by reference, and kept alive by its first item) and the backward's workspace on this device."""
     desc = nat.bconv_block_norm_desc_t(rows, per, width, _DTYPES[dtype], residual_scale, eps)
-    return desc, ctypes.byref(desc), nat.load_library().bconv_block_norm_workspace_bytes(desc)
+    with torch.cuda.device(device):
+        need = nat.load_library().bconv_block_norm_workspace_bytes(desc)
+    return desc, ctypes.byref(desc), need
 
 
 def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_gate, residual_scale, eps):
@@ -250,7 +253,7 @@ def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_ga
         if gates != -(-rows // per):
             raise ValueError(f"{gates} gate rows of {per} rows each do not fit {rows} rows")
         gate = _like(gate, device, dtype, gate.shape, "gate")
-    return residual, block, pre_weight, post_weight, gate, device, (rows, per, width, dtype, residual_scale, eps)
+    return residual, block, pre_weight, post_weight, gate, device, (device, rows, per, width, dtype, residual_scale, eps)
 
 
 def block_norm(residual, block=None, *, pre_weight=None, post_weight=None, gate=None, rows_per_gate=None,
@@ -298,12 +301,7 @@ def block_norm_backward(residual_out, block=None, *, pre_weight=None, post_weigh
                       None if pre_weight is None else _empty_like(pre_weight),
                       None if post_weight is None else _empty_like(post_weight),
                       None if gate is None else _empty_like(gate, dtype=_F32))
-    if device == _current_device():
-        _, desc, need = _norm_desc(*args)
-    else:  # (the workspace goes by the device's SMs)
-        with torch.cuda.device(device):
-            desc = ctypes.byref(nat.bconv_block_norm_desc_t(*args[:3], _DTYPES[dtype], *args[4:]))
-            need = nat.load_library().bconv_block_norm_workspace_bytes(desc)
+    _, desc, need = _norm_desc(*args)
     ws = residual_out.new_empty(max(need, 1), dtype=torch.uint8)
     _call("bconv_block_norm_backward", device, desc, residual_out.data_ptr(), _ptr(block), _ptr(gate),
           _ptr(post_weight), _ptr(pre_weight), _ptr(d_residual_out), _ptr(d_normed), g.d_residual.data_ptr(),
@@ -321,6 +319,7 @@ class TokenLogprobs(NamedTuple):
 
 @functools.lru_cache(maxsize=256)
 def _token_desc(rows, stride, vocab, dtype, top, temperature):
+    """The C descriptor by reference (kept alive by the first item)."""
     desc = nat.bconv_token_desc_t(rows, stride, vocab, _DTYPES[dtype], top, temperature)
     return desc, ctypes.byref(desc)
 

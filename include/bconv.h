@@ -373,7 +373,8 @@ typedef enum { BCONV_DTYPE_F32 = 0, BCONV_DTYPE_BF16 = 1, BCONV_DTYPE_F16 = 2 } 
  *     W[c][f] = scale[c][f / group_size] * (code[c][f] - zero[c][f / group_size])
  *
  * The codes (0..15) enter the sums as exact integers code - zero; each group's sum is scaled
- * in fp32, so the weights themselves are never rounded.
+ * in fp32, so the weights themselves are never rounded, and fp32 inputs enter as three bf16
+ * numbers whose sum they are (an infinite fp32 input makes its row NaN).
  *   in_channels, out_channels  1 .. 2^20.
  *   group_size  32, 64, a multiple of 128, or >= in_channels (one group per output channel);
  *               the last group of a row may be partial.

@@ -213,6 +213,32 @@ def test_quant_fc_streams_and_graphs(rows, dtype):
     del graphs
 
 
+@pytest.mark.parametrize("rows", [1, 7, 50, 300])
+def test_quant_fc_layers_one_after_another(rows):
+    """Layers that read what the layer before wrote, without waiting: a kernel may start, and read its codes, while
+    the one before it still runs, but not its rows."""
+    k = 512
+    cases = [quant_case(i, k, k, 128, True, False) for i in range(4)]
+    layers = [bc.QuantFC(k, k, codes=c[0], scale=c[1], zero=c[2], dtype="bf16") for c in cases]
+    x = rnd(rows, rows, k, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    want = []
+    for _ in range(5):
+        y = x
+        for layer in layers:
+            y = layer(y)
+            torch.cuda.synchronize()
+        want.append(y)
+    a, b = torch.empty_like(x), torch.empty_like(x)  # two buffers in turn: written again while the next layer starts
+    got = []
+    for _ in range(20):
+        a.copy_(x)
+        for i, layer in enumerate(layers):
+            layer.forward_into((a, b)[i % 2], (b, a)[i % 2])
+        got.append(a.clone())
+    assert all(torch.equal(y, want[0]) for y in want + got)
+
+
 def test_quant_fc_past_two_gigabytes_of_offsets():
     """Input and output offsets beyond 2^31 elements (rows far apart)."""
     k, n, rows = 64, 32, 3
@@ -447,6 +473,57 @@ def test_block_norm_many_rows_share_gates():
         got = bc.block_norm_backward(out, b, pre_weight=pre, post_weight=pw, gate=g, rows_per_gate=per, d_normed=d)
         want, mags = norm_grad_ref(*opt64(out, b, pre, pw, g), per, 1.0, 1e-6, None, d.double())
         close(got.d_gate, want["d_gate"], (4 * ROW + 60 * U) * mags["d_gate"])
+
+
+@pytest.mark.parametrize("width", [1024, 1027])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_block_norm_in_place_over_many_rows(width, dtype):
+    """Outputs over their inputs, as the header allows it, where rows are requested ahead of their use."""
+    from binarized_convolution_b200 import _native as nat
+
+    rows, per = 2000, 64
+    r, b, pre, pw, g = norm_inputs(21, rows, width, per, dtype)
+    do, dn = rnd(22, rows, width, dtype=dtype), rnd(23, rows, width, dtype=dtype)
+    kw = dict(pre_weight=pre, post_weight=pw, gate=g, rows_per_gate=per)
+    code = {torch.float32: nat.DTYPE_F32, torch.bfloat16: nat.DTYPE_BF16, torch.float16: nat.DTYPE_F16}[dtype]
+    desc = nat.bconv_block_norm_desc_t(rows, per, width, code, 1.0, 1e-6)
+    s = torch.cuda.current_stream().cuda_stream
+    out, normed = bc.block_norm(r, b, **kw)
+    for first, second in ((0, 1), (1, None)):  # (residual_out over residual, normed over block); residual_out over block
+        r1, b1, free = r.clone(), b.clone(), torch.empty_like(r)
+        to = [r1, b1][first], b1 if second == 1 else free
+        bc.bconv_block_norm_forward(desc, r1.data_ptr(), b1.data_ptr(), g.data_ptr(), pw.data_ptr(), pre.data_ptr(),
+                                    to[0].data_ptr(), to[1].data_ptr(), s)
+        assert torch.equal(to[0], out) and torch.equal(to[1], normed)
+    want = bc.block_norm_backward(out, b, d_residual_out=do, d_normed=dn, **kw)
+    ws = torch.empty(bc.bconv_block_norm_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    for swap in (False, True):
+        d1, d2 = do.clone(), dn.clone()
+        to = (d2, d1) if swap else (d1, d2)
+        sums = [torch.empty_like(x) for x in want[2:]]
+        bc.bconv_block_norm_backward(desc, out.data_ptr(), b.data_ptr(), g.data_ptr(), pw.data_ptr(), pre.data_ptr(),
+                                     d1.data_ptr(), d2.data_ptr(), to[0].data_ptr(), to[1].data_ptr(),
+                                     *[x.data_ptr() for x in sums], ws.data_ptr(), s)
+        assert all(torch.equal(x, y) for x, y in zip((*to, *sums), want))
+
+
+def test_block_norm_backward_asked_for_parts():
+    """Any of the results may be left out, and the workspace where no sum over rows is wanted."""
+    from binarized_convolution_b200 import _native as nat
+
+    for rows, width in ((20, 136), (700, 640)):
+        out, b, pre, pw, g = norm_inputs(31, rows, width, 10, torch.float32)
+        do, dn = rnd(32, rows, width), rnd(33, rows, width)
+        want = bc.block_norm_backward(out, b, pre_weight=pre, post_weight=pw, gate=g, rows_per_gate=10,
+                                      d_residual_out=do, d_normed=dn)
+        desc = nat.bconv_block_norm_desc_t(rows, 10, width, nat.DTYPE_F32, 1.0, 1e-6)
+        ws = torch.empty(bc.bconv_block_norm_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+        for keep in range(5):
+            only = [torch.full_like(x, 7.0) if i == keep else None for i, x in enumerate(want)]
+            bc.bconv_block_norm_backward(desc, out.data_ptr(), b.data_ptr(), g.data_ptr(), pw.data_ptr(), pre.data_ptr(),
+                                         do.data_ptr(), dn.data_ptr(), *[None if x is None else x.data_ptr() for x in only],
+                                         ws.data_ptr() if keep >= 2 else None, torch.cuda.current_stream().cuda_stream)
+            assert torch.equal(only[keep], want[keep]), keep
 
 
 def test_block_norm_refusals():
