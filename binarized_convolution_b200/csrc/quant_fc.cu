@@ -81,18 +81,12 @@ struct bfc_quant_handle_s {
   int device = 0;
   bfc_quant_desc_t desc = {};
   int group = 0, groups = 0, k_tiles = 0, no_pad = 0;
+  void* memory = nullptr;  // one allocation: codes, scales, zeros, bias, error word
   uint4* codes = nullptr;
   float* scale = nullptr;
   uint8_t* zero = nullptr;
   float* bias = nullptr;
   uint32_t* err = nullptr;
-  void release() {
-    cudaFree(codes);
-    cudaFree(scale);
-    cudaFree(zero);
-    cudaFree(bias);
-    cudaFree(err);
-  }
 };
 
 using namespace bconv;
@@ -119,10 +113,19 @@ cudaError_t fill(bfc_quant_handle_s* h, const uint8_t* codes, const float* scale
   void* scratch[3] = {nullptr, nullptr, nullptr};
   const void* src = nullptr;
   const auto blocks = [](int64_t n) { return static_cast<unsigned>(ceil_div(n, 256)); };
-  cudaError_t e = cudaMalloc(&h->codes, tiles * kQuantTileBytes);
-  if (e == cudaSuccess) e = cudaMalloc(&h->scale, per_group * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(uint32_t));
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(uint32_t), nullptr);
+  // (every part 256-byte aligned: the kernels copy tiles and groups of channels with bulk copies)
+  const auto part = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+  const int64_t b_codes = part(tiles * kQuantTileBytes), b_scale = part(per_group * 4), b_zero = zero ? part(per_group) : 0,
+                b_bias = bias ? part(int64_t{no} * 4) : 0;
+  cudaError_t e = cudaMalloc(&h->memory, b_codes + b_scale + b_zero + b_bias + 256);
+  if (e != cudaSuccess) return e;
+  uint8_t* at = static_cast<uint8_t*>(h->memory);
+  h->codes = reinterpret_cast<uint4*>(at);
+  h->scale = reinterpret_cast<float*>(at += b_codes);
+  h->zero = zero ? (at + b_scale) : nullptr;
+  h->bias = bias ? reinterpret_cast<float*>(at + b_scale + b_zero) : nullptr;
+  h->err = reinterpret_cast<uint32_t*>(at + b_scale + b_zero + b_bias);
+  e = cudaMemsetAsync(h->err, 0, sizeof(uint32_t), nullptr);
   if (e == cudaSuccess) e = on_device(codes, static_cast<size_t>(no) * ((k + 1) / 2), h->device, &scratch[0], &src);
   if (e == cudaSuccess) {
     const int64_t pieces = tiles * 4 * kQuantRows;
@@ -136,21 +139,18 @@ cudaError_t fill(bfc_quant_handle_s* h, const uint8_t* codes, const float* scale
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && zero) {
-    e = cudaMalloc(&h->zero, per_group);
-    if (e == cudaSuccess) e = on_device(zero, given, h->device, &scratch[2], &src);
+    e = on_device(zero, given, h->device, &scratch[2], &src);
     if (e == cudaSuccess) {
       quant_transpose_kernel<uint8_t>
           <<<blocks(per_group), 256>>>(static_cast<const uint8_t*>(src), no, h->no_pad, h->groups, uint8_t{15}, h->zero);
       e = cudaGetLastError();
     }
   }
-  if (e == cudaSuccess && bias) {
-    e = cudaMalloc(&h->bias, no * sizeof(float));
-    if (e == cudaSuccess) e = cudaMemcpy(h->bias, bias, no * sizeof(float), cudaMemcpyDefault);
-  }
+  if (e == cudaSuccess && bias) e = cudaMemcpy(h->bias, bias, no * sizeof(float), cudaMemcpyDefault);
   // the arrays are read during the call only, and any stream may use the handle afterwards
   const cudaError_t done = cudaStreamSynchronize(nullptr);
-  for (void* p : scratch) cudaFree(p);
+  for (void* p : scratch)
+    if (p) cudaFree(p);
   return e != cudaSuccess ? e : done;
 }
 
@@ -189,7 +189,7 @@ bconv_status_t bfc_quant_create(const bfc_quant_desc_t* d, const uint8_t* codes,
   if (e != cudaSuccess) {
     cudaGetLastError();
     h->magic = 0;
-    h->release();
+    cudaFree(h->memory);
     delete h;
     return from_cuda(e);
   }
@@ -243,7 +243,7 @@ bconv_status_t bfc_quant_destroy(bfc_quant_handle_t h) {
   if (!g.ok) return BCONV_ERR_CUDA;
   const cudaError_t e = cudaDeviceSynchronize();
   h->magic = 0;
-  h->release();
+  cudaFree(h->memory);
   delete h;
   return from_cuda(e);
 }
