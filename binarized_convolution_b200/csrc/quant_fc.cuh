@@ -33,11 +33,14 @@ struct QuantFcArgs {
   int relu;
 };
 
-// Codes less zeros: `v` two 4-bit numbers in the halves of a word, or-ed into 1024.0 (fp16) or 128.0 (bf16), whose
-// last significant bits are worth 1; `zero` that constant plus the zero, twice.  Exact.
+// Codes less zeros: two 4-bit numbers of w, in the low bits of its halves, or-ed into 1024.0 (fp16) or 128.0
+// (bf16), whose last significant bits are worth 1, less `zero`, that constant plus the zero, twice.  Exact.  One
+// three-operand logic instruction takes the bits out and puts them in (two constants at once are more than
+// an instruction can name, so one is given in a register).
 template <bool HALF>
-__device__ __forceinline__ uint32_t decode(uint32_t v, uint32_t zero) {
-  const uint32_t a = v | (HALF ? 0x64006400u : 0x43004300u);
+__device__ __forceinline__ uint32_t decode(uint32_t w, uint32_t zero) {
+  uint32_t a;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a) : "r"(w), "r"(0x000f000fu), "r"(HALF ? 0x64006400u : 0x43004300u));
   if (HALF) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&zero));
     return *reinterpret_cast<const uint32_t*>(&r);

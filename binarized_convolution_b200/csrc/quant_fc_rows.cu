@@ -50,16 +50,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // A tile of 128 input channels of this lane's two channels.
-template <int UNITS>
+template <int UNITS, bool ZERO>
 struct Item {
   uint4 w[2];
   float s[2][UNITS];
-  uint32_t z[2][UNITS];
+  uint32_t z[2][ZERO ? UNITS : 1];
 };
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
 // T: element type of the rows; PARTS: 1, or 3 bf16 parts of fp32; NT: tiles of 8 tokens; UNITS: groups per 128
-// input channels.
-template <typename T, int PARTS, int NT, int UNITS>
+// input channels; ZERO: whether the layer has zeros (else they are 8).
+template <typename T, int PARTS, int NT, int UNITS, bool ZERO>
 __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsArgs a, int out_dtype) {
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr uint32_t kBias = HALF ? 0x6400u : 0x4300u;  // 1024.0 or 128.0: or-ing a 4-bit number in adds it
@@ -73,10 +79,11 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
 
   // items: tile after tile, nk steps each.  The addresses of the next one to load move on by additions.
   const int stride = gridDim.x * teams, first = blockIdx.x * teams + team;
-  Item<UNITS> ring[kDepth];
+  Item<UNITS, ZERO> ring[kDepth];
   int l_tile = first, l_k = 0, l_group = 0, l_left = 0;  // l_left: steps until the next group (one unit)
   const uint4* l_codes = nullptr;
-  int64_t l_terms = 0;  // of the scales and zeros
+  const float* l_scale = nullptr;
+  const uint8_t* l_zero = nullptr;
   const int last_group = (a.q.k + a.q.group - 1) / a.q.group - 1;
   const int steps_per_group = a.q.group / kQuantK;  // (one unit)
   auto start_tile = [&]() {
@@ -85,24 +92,29 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
               t * kQuantRows + row % kQuantRows;
     l_group = UNITS == 1 ? kt0 / steps_per_group : kt0 * UNITS;
     l_left = UNITS == 1 ? steps_per_group - (kt0 - l_group * steps_per_group) : 0;
-    l_terms = static_cast<int64_t>(min(l_group, last_group)) * a.q.no_pad + row;
+    const int64_t terms = static_cast<int64_t>(min(l_group, last_group)) * a.q.no_pad + row;
+    l_scale = a.q.scale + terms;
+    if (ZERO) l_zero = a.q.zero + terms;
   };
-  auto load = [&](Item<UNITS>& it) {
+  auto load = [&](Item<UNITS, ZERO>& it) {
     if (l_tile >= a.tiles) return;
     it.w[0] = __ldcs(l_codes);
     it.w[1] = __ldcs(l_codes + 8);
     l_codes += kQuantTileBytes / 16;
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
-      it.s[0][u] = __ldg(a.q.scale + l_terms);
-      it.s[1][u] = __ldg(a.q.scale + l_terms + 8);
-      if (a.q.zero) {
-        it.z[0][u] = a.q.zero[l_terms];
-        it.z[1][u] = a.q.zero[l_terms + 8];
+      it.s[0][u] = __ldg(l_scale);
+      it.s[1][u] = __ldg(l_scale + 8);
+      if (ZERO) {
+        it.z[0][u] = __ldg(l_zero);
+        it.z[1][u] = __ldg(l_zero + 8);
       }
       // (behind the last group the inputs are 0)
       if (UNITS > 1 || --l_left == 0) {
-        if (l_group++ < last_group) l_terms += a.q.no_pad;
+        if (l_group++ < last_group) {
+          l_scale += a.q.no_pad;
+          if (ZERO) l_zero += a.q.no_pad;
+        }
         l_left = steps_per_group;
       }
     }
@@ -114,10 +126,6 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   };
   if (nk == 0) l_tile = a.tiles;
   start_tile();
-#pragma unroll
-  for (int i = 0; i < kDepth; ++i)
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) ring[i].z[0][u] = ring[i].z[1][u] = 8u;
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) load(ring[i]);
 
@@ -175,13 +183,14 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   const int turns = (a.tiles - static_cast<int>(blockIdx.x) * teams + stride - 1) / stride;  // of the CTA's first team
   int tile = first, k = 0;
   // this lane's B operands: row n * 8 + g, or zeros (256 bytes behind the rows) where there is no such row
-  const uint8_t *x_start[NT], *x_at[NT];
-  int x_step[NT];
+  uint32_t x_start[NT], x_at[NT], x_step[NT], x_plane[NT];
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool real = n * 8 + g < rows;
-    x_start[n] = x_at[n] = real ? smem + (n * 8 + g) * a.pitch + (kt0 * kQuantK + 8 * t) * 2 : smem + PARTS * rows * a.pitch + 16 * t;
+    x_start[n] = x_at[n] = base + (real ? (n * 8 + g) * a.pitch + (kt0 * kQuantK + 8 * t) * 2 : PARTS * plane + 16 * t);
     x_step[n] = real ? kQuantK * 2 : 0;
+    x_plane[n] = real ? plane : 0;
   }
 
   auto finish = [&]() {  // the tile's sums are complete (nothing in warps without input channels)
@@ -219,11 +228,12 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
     tile += stride;
   };
 
-  auto step = [&](const Item<UNITS>& it) {
+  auto step = [&](const Item<UNITS, ZERO>& it) {
     const uint32_t w[2][4] = {{it.w[0].x, it.w[0].y, it.w[0].z, it.w[0].w}, {it.w[1].x, it.w[1].y, it.w[1].z, it.w[1].w}};
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
-      const uint32_t zz[2] = {(kBias | it.z[0][u]) * 0x10001u, (kBias | it.z[1][u]) * 0x10001u};
+      const uint32_t zz[2] = {ZERO ? (kBias | it.z[0][u]) * 0x10001u : (kBias | 8u) * 0x10001u,
+                              ZERO ? (kBias | it.z[1][u]) * 0x10001u : (kBias | 8u) * 0x10001u};
       float d[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -235,13 +245,13 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[r][i] = decode<HALF>((w[r][c] >> (4 * i)) & 0x000f000fu, zz[r]);
+          for (int i = 0; i < 4; ++i) p[r][i] = decode<HALF>(w[r][c] >> (4 * i), zz[r]);
         const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]}, a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint4 b = *reinterpret_cast<const uint4*>(x_at[n] + (x_step[n] ? part * plane : 0) + c * 64);
+            const uint4 b = lds128(x_at[n] + part * x_plane[n] + c * 64);
             mma16816<HALF>(d[n], a0, b.x, b.y);
             mma16816<HALF>(d[n], a1, b.z, b.w);
           }
@@ -280,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   }
 }
 
-template <typename T, int PARTS, int NT, int UNITS>
+template <typename T, int PARTS, int NT, int UNITS, bool ZERO>
 cudaError_t launch(const RowsArgs& a, int out_dtype, int ctas, int smem, cudaStream_t s) {
-  auto kern = quant_fc_rows_kernel<T, PARTS, NT, UNITS>;
-  const cudaError_t set = allow_smem<quant_fc_rows_kernel<T, PARTS, NT, UNITS>>(kMaxSmem);
+  auto kern = quant_fc_rows_kernel<T, PARTS, NT, UNITS, ZERO>;
+  const cudaError_t set = allow_smem<quant_fc_rows_kernel<T, PARTS, NT, UNITS, ZERO>>(kMaxSmem);
   if (set != cudaSuccess) return set;
   const cudaError_t e = launch_overlapped(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, s, a, out_dtype);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -326,11 +336,15 @@ cudaError_t launch_quant_fc_rows(const QuantFcArgs& q, int in_dtype, int out_dty
   const auto with_units = [&](auto t, auto parts, auto nt) {
     using T = decltype(t);
     constexpr int kParts = decltype(parts)::value, kNt = decltype(nt)::value;
-    switch (units) {
-      case 1: return launch<T, kParts, kNt, 1>(a, out_dtype, ctas, smem, s);
-      case 2: return launch<T, kParts, kNt, 2>(a, out_dtype, ctas, smem, s);
-      default: return launch<T, kParts, kNt, 4>(a, out_dtype, ctas, smem, s);
-    }
+    const auto with_zero = [&](auto has) {
+      constexpr bool kZero = decltype(has)::value;
+      switch (units) {
+        case 1: return launch<T, kParts, kNt, 1, kZero>(a, out_dtype, ctas, smem, s);
+        case 2: return launch<T, kParts, kNt, 2, kZero>(a, out_dtype, ctas, smem, s);
+        default: return launch<T, kParts, kNt, 4, kZero>(a, out_dtype, ctas, smem, s);
+      }
+    };
+    return q.zero ? with_zero(std::true_type{}) : with_zero(std::false_type{});
   };
   using One = std::integral_constant<int, 1>;
   using Two = std::integral_constant<int, 2>;

@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < 4; ++p)
               v[c * 16 + t * 4 + p] =
-                  decode<HALF>((w[t][2 * two + c] >> (4 * p)) & 0x000f000fu, zz[2 * two + c]);
+                  decode<HALF>(w[t][2 * two + c] >> (4 * p), zz[2 * two + c]);
         if (two == 0) {  // the place is free when the MMAs of step i - a_stages are done
           if (i >= a.a_stages) {
             ok = wait_warp(done + 8 * ds, dph, B, err);
