@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   constexpr uint32_t kBias = HALF ? 0x6400u : 0x4300u;  // 1024.0 or 128.0: or-ing a 4-bit number in adds it
   constexpr int kDepth = UNITS == 1 ? 4 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // [part][row][pitch], 256 bytes of zeros
-  __shared__ float sums[kWarps][NT * 4][32];
+  __shared__ float sums[2][kWarps][NT * 4][32];  // used in turn, so that one barrier a tile is enough
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = static_cast<int>(a.q.rows);
   const int share = warp % a.ksplit, team = warp / a.ksplit, teams = kWarps / a.ksplit;
@@ -193,13 +193,14 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
     x_plane[n] = real ? plane : 0;
   }
 
+  int turn = 0;
   auto finish = [&]() {  // the tile's sums are complete (nothing in warps without input channels)
     const bool real = tile < a.tiles;
     if (a.ksplit > 1) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sums[warp][n * 4 + i][lane] = acc[n][i];
+        for (int i = 0; i < 4; ++i) sums[turn][warp][n * 4 + i][lane] = acc[n][i];
       __syncthreads();
     }
     if (share == 0 && real) {
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float v = acc[n][i];
-          for (int p = 1; p < a.ksplit; ++p) v += sums[warp + p][n * 4 + i][lane];
+          for (int p = 1; p < a.ksplit; ++p) v += sums[turn][warp + p][n * 4 + i][lane];
           const int c = tile * 16 + g + (i >= 2 ? 8 : 0), row = n * 8 + 2 * t + (i & 1);
           if (c < a.q.no && row < rows) {
             if (a.q.bias) v += __ldg(a.q.bias + c);
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
           }
         }
     }
-    if (a.ksplit > 1) __syncthreads();
+    turn ^= 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -243,9 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
       for (int c = u * (4 / UNITS); c < (u + 1) * (4 / UNITS); ++c) {
         uint32_t p[2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[r][i] = decode<HALF>(w[r][c] >> (4 * i), zz[r]);
+        for (int r = 0; r < 2; ++r) decode<HALF>(w[r][c], zz[r], p[r]);
         const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]}, a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)

@@ -472,11 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t) {
+            uint32_t p[4];
+            decode<HALF>(w[t][2 * two + c], zz[2 * two + c], p);
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-              v[c * 16 + t * 4 + p] =
-                  decode<HALF>(w[t][2 * two + c] >> (4 * p), zz[2 * two + c]);
+            for (int i = 0; i < 4; ++i) v[c * 16 + t * 4 + i] = p[i];
+          }
         if (two == 0) {  // the place is free when the MMAs of step i - a_stages are done
           if (i >= a.a_stages) {
             ok = wait_warp(done + 8 * ds, dph, B, err);
