@@ -18,11 +18,13 @@
 //
 // Roles (20 warps): warp 0 loads the tokens (TMA boxes of 64 input channels x N tokens) and the scales,
 // warp 1 issues the MMAs, warp 2 loads the codes, warps 4-7 and 8-11 decode every second tile,
-// warps 12-15 and 16-19 take the groups' sums out of TMEM: those of one half of the tokens each, or,
-// up to 96 tokens, of every second group.  Each of these two has two accumulator slots, so that one sum
-// is taken out while the next one is formed.  What the one MMA-issuing thread does between two
-// tiles is on the critical path, so it has few barriers: one per tile for everything that the MMAs
-// read (tokens, scales, codes) and one for its release, and two per accumulator slot.
+// warps 12-15 and 16-19 take the groups' sums out of TMEM: up to 96 tokens those of every second group
+// each, with two accumulators each; above, half of the tokens of every group each, with two accumulators
+// in turn, so that one sum is taken out while the next one is formed.  The one thread that issues the MMAs is
+// on the critical path: up to 64 tokens a tile takes it about 600 of the 800 cycles that the tile takes in all.  So
+// the MMAs are few and large (160 x 4096 x 16384 bf16: 28.9 us with MMAs of 160 tokens, 30.9 with two of
+// 80), and the barriers few: one per tile for everything that the MMAs read (tokens, scales, codes) and
+// one for its release, and two per accumulator.
 // A CTA walks over its tiles without a pause: tokens and codes of the next one are on their way and decoded
 // while the sums of the last are written (a CTA per tile spent 8 us a tile outside its loop over
 // the input channels: 44 of 140 us for 2000 x 4096 x 8192).  Where there are few tiles, a cluster of CTAs
@@ -52,8 +54,8 @@ constexpr int kThreads = 640;
 constexpr int kWStages = 6;          // tiles of codes in flight
 constexpr int kMaxStages = 8;        // tiles of tokens in flight
 constexpr int kScaleSlack = 4;       // the scales of a tile are used up to so many tiles after its tokens
-constexpr int kMaxCols = 96;         // tokens of an MMA
-constexpr int kSlots = 4;            // accumulators
+constexpr int kMaxCols = 96;         // tokens whose sums a warp takes out; two warpgroups may share an MMA's
+constexpr int kSlots = 4;            // accumulators of up to kMaxCols tokens, or two of twice as many
 constexpr int kACols = kQuantK / 2;  // TMEM columns of a decoded tile
 constexpr int kTmemCols = 512;
 static_assert(kSlots * kMaxCols + 2 * kACols <= kTmemCols, "TMEM: a decoded tile of each decoding warpgroup at least");
@@ -75,14 +77,14 @@ constexpr int kRingBytes = (kSmemBytes - static_cast<int>(sizeof(Bars))) / 1024 
 
 struct TcQuantArgs {
   QuantFcArgs q;
-  int cols;        // tokens of an MMA (a multiple of 16, at most kMaxCols)
+  int cols;        // tokens of an MMA: a multiple of 16 up to kMaxCols, or of 32 up to twice that
   int slot_cols;   // TMEM columns between the accumulators
   int a_stages;    // decoded tiles in TMEM (even: the decoding warpgroups take turns)
   int parts;       // bf16 parts of the input (3 for fp32), multiplied one after the other
   int fold;        // or 3 parts as rows of their own, whose sums are added up at the end
   int part_rows;   // rows between the parts in the tensor map
   int stages;      // tiles of tokens in flight
-  int tiles;       // of 128 channels x HALVES * cols tokens
+  int tiles;       // of 128 channels x cols tokens
   int exchange;    // bytes for the sums of the second stream (one half of tokens, CTAs of several tiles)
   int units;       // groups per 128 input channels (1 for groups of 128 and more)
   int splits;      // CTAs of a cluster sharing a tile
@@ -227,8 +229,8 @@ __device__ __forceinline__ void put4(T* to, const float (&y)[4], int left) {
   }
 }
 
-// HALVES: halves of the tokens (a CTA has HALVES * cols tokens); HALF: fp16 operands, else bf16; UNITS:
-// groups per 128 input channels.
+// HALVES: 1: the warpgroups that take sums out take every second group each, 2: half of the tokens each; HALF:
+// fp16 operands, else bf16; UNITS: groups per 128 input channels.
 template <int HALVES, bool HALF, int UNITS>
 __global__ void __launch_bounds__(kThreads, 1)
     quant_fc_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ TcQuantArgs a) {
@@ -260,9 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int my_tiles = tile0 < a.tiles ? (a.tiles - tile0 + tile_step - 1) / tile_step : 0;
   const int steps = my_tiles * n;
   const bool joined = a.splits > 1 || a.fold > 1;  // sums that meet in shared memory (one tile a CTA)
-  const int piece_bytes = a.cols * kQuantK * 2;     // [64-channel block][token][128 bytes]
-  const int pieces = HALVES * a.parts;              // of a tile: halves of the tokens or parts of the input
-  const int stage_b = pieces * piece_bytes;
+  const int piece_bytes = a.cols * kQuantK * 2;     // of a tile and part: [64-channel block][token][128 bytes]
+  const int stage_b = a.parts * piece_bytes;
   const uint32_t bars = smem_u32(B);
   const uint32_t ready = bars + offsetof(Bars, ready), done = bars + offsetof(Bars, done);
   const uint32_t full_w = bars + offsetof(Bars, full_w), empty_w = bars + offsetof(Bars, empty_w);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&B->full_d[i], 1);
-      mbar_init(&B->empty_d[i], 4);
+      mbar_init(&B->empty_d[i], HALVES * 4);
     }
     mbar_init(&B->last, 1);
     B->abort_flag = 0;
@@ -295,12 +296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_base;
-  const uint32_t tmem_a = tmem + static_cast<uint32_t>(kSlots * a.slot_cols);
-  const int groups = (a.q.k + a.q.group - 1) / a.q.group;
-  // first of a tile's channels in a [groups][no_pad] array (behind the last group the inputs are 0)
-  auto group_at = [&](int rt, int i, int u) {
-    const int g = min(((kt0 + i) * kQuantK + u * kGroup) / a.q.group, groups - 1);
-    return static_cast<int64_t>(g) * a.q.no_pad + rt * kQuantRows;
+  const uint32_t tmem_a = tmem + static_cast<uint32_t>(kSlots / HALVES * a.slot_cols);
+  // The groups of a tile's steps, in order, as offsets of the tile's channels in a [groups][no_pad] array (counted, so
+  // that the copying threads divide once a tile).  Behind the last group the inputs are 0.
+  const int last_group = (a.q.k + a.q.group - 1) / a.q.group - 1, steps_per_group = max(a.q.group / kQuantK, 1);
+  struct Groups {
+    int64_t at;
+    int group, left;
+  };
+  auto first_group = [&](int rt) {
+    const int g = UNITS == 1 ? kt0 / steps_per_group : kt0 * UNITS;
+    return Groups{static_cast<int64_t>(min(g, last_group)) * a.q.no_pad + rt * kQuantRows, g,
+                  UNITS == 1 ? steps_per_group - (kt0 - g * steps_per_group) : 1};
+  };
+  auto next_group = [&](Groups& g) {
+    if (--g.left == 0) {
+      if (g.group++ < last_group) g.at += a.q.no_pad;
+      g.left = steps_per_group;
+    }
   };
 
   // The launch has 96 registers a thread, 5 x 96 in all: 40 + 2 x 72 + 2 x 144.
@@ -315,21 +328,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = static_cast<uint32_t>(stage_b + kScaleBytes);
         bool ok = true;
         for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-          const int rt = tile % row_tiles, token0 = tile / row_tiles * (HALVES * a.cols);
-          for (int i = 0; i < n; ++i) {
+          const int rt = tile % row_tiles, token0 = tile / row_tiles * a.cols;
+          Groups group = first_group(rt);
+          int c = kt0 * kQuantK;
+          for (int i = 0; i < n; ++i, c += kQuantK) {
             if (!(ok = wait(done + 8 * s, phase, B, err))) break;
             mbar_expect_tx(&B->ready[s], bytes);
             uint8_t* to = ring_b + s * stage_b;
-            int at = token0;
-            const int c = (kt0 + i) * kQuantK;
-            for (int p = 0; p < pieces; ++p, to += piece_bytes) {
+            for (int p = 0, at = token0; p < a.parts; ++p, to += piece_bytes, at += a.part_rows) {
               tma_load_2d(to, &tmB, &B->ready[s], c, at);
               tma_load_2d(to + a.cols * 128, &tmB, &B->ready[s], c + 64, at);
-              at += HALVES == 2 ? a.cols : a.part_rows;
             }
-            for (int u = 0; u < UNITS; ++u)
-              bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group_at(rt, i, u), kQuantRows * 4,
-                        &B->ready[s]);
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+              bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group.at, kQuantRows * 4, &B->ready[s]);
+              next_group(group);
+            }
             ++issued;
             if (++ss == scale_stages) ss = 0;
             if (++s == a.stages) {
@@ -352,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t desc_piece = static_cast<uint32_t>(piece_bytes) >> 4;
         const uint32_t desc_block = static_cast<uint32_t>(a.cols) * 8u;
         uint32_t desc = desc0, ready_ph = 0;
-        // slot: 2 * stream + turn; streams: the halves of the tokens, or every second unit
+        // slot: 2 * stream + turn (streams: every second unit), or turn
         uint32_t turn = 0, empty_ph = 1, stream = 0;
         int s = 0, as = 0;
         bool ok = true;
@@ -362,23 +376,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++as == a.a_stages) as = 0;
 #pragma unroll
           for (int u = 0; u < UNITS; ++u) {
+            const uint32_t slot = HALVES == 2 ? turn : 2u * stream + turn;
+            if (!ok || !(ok = wait(empty_d + 8 * slot, empty_ph, B, err))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + slot * static_cast<uint32_t>(a.slot_cols);
+            uint32_t lo = desc;
+            for (int p = 0; p < a.parts; ++p, lo += desc_piece) {
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-              const uint32_t slot = 2u * (HALVES == 2 ? h : stream) + turn;
-              if (!ok || !(ok = wait(empty_d + 8 * slot, empty_ph, B, err))) break;
-              tc_fence_after();
-              const uint32_t d = tmem + slot * static_cast<uint32_t>(a.slot_cols);
-              for (int p = 0; p < a.parts; ++p) {
-                const uint32_t lo = desc + (HALVES == 2 ? h : p) * desc_piece;
-#pragma unroll
-                for (int k = u * kSteps; k < (u + 1) * kSteps; ++k) {
-                  const uint32_t b = lo + (k >= kBlockSteps ? desc_block : 0u) + (k % kBlockSteps) * 2u;
-                  if (k == u * kSteps) mma_ts(d, a_tmem + k * 8, b, idesc, p > 0);
-                  else mma_ts<true>(d, a_tmem + k * 8, b, idesc);
-                }
+              for (int k = u * kSteps; k < (u + 1) * kSteps; ++k) {
+                const uint32_t b = lo + (k >= kBlockSteps ? desc_block : 0u) + (k % kBlockSteps) * 2u;
+                if (k == u * kSteps) mma_ts(d, a_tmem + k * 8, b, idesc, p > 0);
+                else mma_ts<true>(d, a_tmem + k * 8, b, idesc);
               }
-              commit(full_d + 8 * slot);
             }
+            commit(full_d + 8 * slot);
             if (HALVES == 1) stream ^= 1u;
             if (HALVES == 2 || stream == 0) {
               turn ^= 1u;
@@ -413,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rt = tile % row_tiles;
           const uint8_t* from = reinterpret_cast<const uint8_t*>(a.q.codes) +
                                 (static_cast<int64_t>(rt) * a.q.k_tiles + kt0) * kQuantTileBytes;
+          Groups group = first_group(rt);
           for (int i = 0; i < n; ++i, from += kQuantTileBytes) {
             if (!(ok = wait(empty_w + 8 * s, phase, B, err))) break;
             ++issued;
@@ -420,8 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(&B->full_w[s], static_cast<uint32_t>(stage_w));
             bulk_load(to, from, kQuantTileBytes, &B->full_w[s]);
             if (a.q.zero)
-              for (int u = 0; u < UNITS; ++u)
-                bulk_load(to + kQuantTileBytes + u * kQuantRows, a.q.zero + group_at(rt, i, u), kQuantRows, &B->full_w[s]);
+#pragma unroll
+              for (int u = 0; u < UNITS; ++u) {
+                bulk_load(to + kQuantTileBytes + u * kQuantRows, a.q.zero + group.at, kQuantRows, &B->full_w[s]);
+                next_group(group);
+              }
             if (++s == kWStages) {
               s = 0;
               phase ^= 1u;
@@ -506,8 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ---------------- sums of groups -> registers ----------------
     const int stream = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t from = tmem + static_cast<uint32_t>(2 * stream * a.slot_cols) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int chunks = a.cols / 16;
+    const int half = HALVES == 2 ? a.cols / 2 : a.cols;  // tokens of this stream
+    const uint32_t from = tmem + static_cast<uint32_t>(stream * (HALVES == 2 ? half : 2 * a.slot_cols)) +
+                          (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int chunks = half / 16;
     bool ok = true;
     uint32_t turn = 0, phase = 0;
     const float* scale = reinterpret_cast<const float*>(ring_s) + row;
@@ -524,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                              : ring_b);
     for (int tile = tile0; tile < a.tiles; tile += tile_step) {
       const int rt = tile % row_tiles;
-      const int64_t token0 = static_cast<int64_t>(tile / row_tiles) * (HALVES * a.cols);
+      const int64_t token0 = static_cast<int64_t>(tile / row_tiles) * a.cols;
       uint64_t acc[kMaxCols / 2];  // pairs of neighbouring tokens, for the packed multiply-add
 #pragma unroll
       for (int j = 0; j < kMaxCols / 2; ++j) acc[j] = 0;
       for (; unit < units && ok; unit += HALVES == 2 ? 1 : 2) {
-        const uint32_t slot = 2u * stream + turn;
+        const uint32_t slot = HALVES == 2 ? turn : 2u * stream + turn;
         if (!(ok = wait_warp(full_d + 8 * slot, phase, B, err))) break;
         tc_fence_after();
         const uint32_t sc = __float_as_uint(scale[(ss * UNITS + u) * kQuantRows]);
@@ -577,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !joined && (HALVES == 2 || stream == 0)) {
         // a lane's channel, token by token: a warp writes 32 neighbouring channels
         const int chan = rt * kQuantRows + row;
-        const int64_t first = token0 + (HALVES == 2 ? stream * a.cols : 0);
-        const int count = static_cast<int>(min(static_cast<int64_t>(a.cols), a.q.rows - first));
+        const int64_t first = token0 + (HALVES == 2 ? stream * half : 0);
+        const int count = static_cast<int>(min(static_cast<int64_t>(half), a.q.rows - first));
         if (chan < a.q.no) {
           const float bias = a.q.bias ? __ldg(a.q.bias + chan) : 0.f;
           auto write = [&](auto* out) {
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one tile: this CTA's sums as [token][channel] over the token ring (all MMAs that read it are done), so
         // that a warp adds up and writes 128 channels of a token at a time
         named_barrier(256);
-        float* const mine = reinterpret_cast<float*>(ring_b) + (HALVES == 2 ? stream * a.cols * kQuantRows : 0) + row;
+        float* const mine = reinterpret_cast<float*>(ring_b) + (HALVES == 2 ? stream * half * kQuantRows : 0) + row;
         if (HALVES == 2 || stream == 0)
 #pragma unroll
           for (int c = 0; c < kMaxCols / 16; ++c)
@@ -632,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !*reinterpret_cast<volatile uint32_t*>(&B->abort_flag)) {
         // tokens split, split + splits, ... of the tile, the warps taking turns; four channels a lane
         const int rt = tile0 % row_tiles;
-        const int64_t token0 = static_cast<int64_t>(tile0 / row_tiles) * (HALVES * a.cols);
+        const int64_t token0 = static_cast<int64_t>(tile0 / row_tiles) * a.cols;
         const int w = warp - 12, c0 = rt * kQuantRows + lane * 4;
         float bias[4] = {0.f, 0.f, 0.f, 0.f};
         if (a.q.bias)
@@ -640,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
             if (c0 + i < a.q.no) bias[i] = __ldg(a.q.bias + c0 + i);
 #pragma unroll 1
-        for (int j = split + w * a.splits; j < HALVES * a.cols; j += 8 * a.splits) {
+        for (int j = split + w * a.splits; j < a.cols; j += 8 * a.splits) {
           const int64_t token = token0 + j;
           if (token >= a.q.rows) break;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -726,19 +743,19 @@ Plan plan_for(const QuantFcArgs& q, int64_t rows, int parts, int most_halves, bo
   constexpr int kFloor = 600;
   const int sms = current_sm_count();
   const int row_tiles = q.no_pad / kQuantRows;
-  const int most_cols = parts == 1 ? kMaxCols : 64;  // (the parts' stages take the space)
+  const int most = parts == 1 ? kMaxCols : 64;  // (the parts' stages take the space)
   Plan best{};
   double best_cost = 1e300;
   for (int halves = 1; halves <= most_halves; ++halves) {
-    const int64_t least = ceil_div(rows, most_cols * halves);
+    const int64_t least = ceil_div(rows, most * halves);
     for (int64_t t = least; t < least + (one_tile ? 1 : 6); ++t) {
-      const int cols = round_up(static_cast<int>(ceil_div(ceil_div(rows, t), halves)), 16);
-      const int64_t tiles = ceil_div(rows, halves * cols) * row_tiles;
+      const int cols = round_up(static_cast<int>(ceil_div(rows, t)), 16 * halves);
+      const int64_t tiles = ceil_div(rows, cols) * row_tiles;
       int splits = 1;
       while (splits < kMaxSplit && tiles * splits * 2 <= sms && q.k_tiles >= splits * 4) splits *= 2;
-      const double per = std::max(4.0 * halves * cols * parts, static_cast<double>(kFloor));
+      const double per = std::max(4.0 * cols * parts, static_cast<double>(kFloor));
       const double cost = static_cast<double>(ceil_div(tiles * splits, sms)) *
-                          (per * static_cast<double>(ceil_div(q.k_tiles, splits)) + 1000.0 + 8.0 * halves * cols);
+                          (per * static_cast<double>(ceil_div(q.k_tiles, splits)) + 1000.0 + 8.0 * cols);
       if (cost < best_cost) {
         best_cost = cost;
         best = {halves, cols, 0, splits, 0, tiles};
@@ -749,7 +766,7 @@ Plan plan_for(const QuantFcArgs& q, int64_t rows, int parts, int most_halves, bo
   const int scale = units * kQuantRows * 4;
   best.exchange = best.halves == 1 && best.tiles > sms ? best.cols * kQuantRows * 4 : 0;
   const int left = kRingBytes - kWStages * w_stage_bytes(units, q.zero) - kScaleSlack * scale - best.exchange;
-  best.stages = std::min(kMaxStages, left / (best.halves * parts * best.cols * kQuantK * 2 + scale));
+  best.stages = std::min(kMaxStages, left / (parts * best.cols * kQuantK * 2 + scale));
   return best;
 }
 
@@ -823,7 +840,7 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   // What the accumulators leave of TMEM holds decoded tiles, but no more of them than tokens: step i arrives on
   // the barrier of step i - stages, whose phase must be over.
   a.slot_cols = round_up(p.cols, 32);
-  a.a_stages = std::min((kTmemCols - kSlots * a.slot_cols) / kACols, p.stages) / 2 * 2;
+  a.a_stages = std::min((kTmemCols - kSlots / p.halves * a.slot_cols) / kACols, p.stages) / 2 * 2;
   a.parts = parts;
   a.fold = fold ? 3 : 1;
   a.part_rows = static_cast<int>(q.rows);
@@ -834,7 +851,7 @@ cudaError_t launch_quant_fc_tc(const QuantFcArgs& q, int in_dtype, int out_dtype
   a.splits = p.splits;
   a.out_dtype = out_dtype;
   a.staged = staged;
-  if (a.stages < 2 || a.a_stages < 2 || a.cols > kMaxCols) return cudaErrorInvalidValue;
+  if (a.stages < 2 || a.a_stages < 2 || a.cols > kMaxCols * p.halves) return cudaErrorInvalidValue;
   auto enc = encoder();
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap map;
