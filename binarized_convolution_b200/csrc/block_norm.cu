@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "dtype.cuh"
+#include "f32x2.cuh"
 #include "host_util.cuh"
 #include "tc_device.cuh"
 
@@ -30,102 +31,102 @@ namespace {
 constexpr int kMaxWidth = 32768;
 constexpr int kSumRows = 16;  // partial rows a column of the final sums is split over
 
-// Where a thread's 8 * j + e-th channel of a row is: with VEC, 8 consecutive channels per j (16-byte
-// accesses; C % 8 == 0 and every row 16-byte aligned), else one channel per access, a warp's side
-// by side.
-template <bool VEC>
-__device__ __forceinline__ int channel(int j, int e, int t) {
+// Where the 8 * j + e-th of a thread's NV * 8 channels of a row is: with VEC, 8 consecutive channels per j (16-byte
+// accesses; C % 8 == 0 and every row 16-byte aligned), else one channel per access, a warp's side by side and
+// its NV * 256 channels together, so that j and e only add constants and all warps but the last have whole rows
+// (an address and a bound per channel were two thirds of the instructions for odd widths).
+template <bool VEC, int NV>
+__device__ __forceinline__ int channel(int j, int e) {
   const int i = static_cast<int>(threadIdx.x);
-  return VEC ? (j * t + i) * 8 + e : (j * 8 + e) * t + i;
+  return VEC ? (j * static_cast<int>(blockDim.x) + i) * 8 + e : (i >> 5) * (NV * 256) + (i & 31) + (j * 8 + e) * 32;
+}
+// Whether all of a thread's channels are there (the same for a whole warp).
+template <int NV>
+__device__ __forceinline__ bool whole(int C) {
+  return (static_cast<int>(threadIdx.x >> 5) + 1) * (NV * 256) <= C;
 }
 
-// (t: the threads that share a row)
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int j, int C, float (&v)[8], int t = blockDim.x) {
+template <bool VEC, int NV, typename T>
+__device__ __forceinline__ void load8(const T* row, int j, int C, float (&v)[8]) {
+  const int c0 = channel<VEC, NV>(j, 0);
   if (VEC) {
-    const int c = channel<true>(j, 0, t);
-    if (c < C) {
+    if (c0 < C) {
       Raw8<T> w;
-      w.load(row + c);
+      w.load(row + c0);
       w.unpack(v);
       return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
   } else {
+    const T* const p = row + c0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = channel<false>(j, e, t);
-      v[e] = c < C ? to_f32(row[c]) : 0.f;
-    }
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e * 32 < C ? to_f32(p[e * 32]) : 0.f;
   }
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8], int t = blockDim.x) {
+template <bool VEC, int NV, typename T>
+__device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8]) {
+  const int c0 = channel<VEC, NV>(j, 0);
   if (VEC) {
-    const int c = channel<true>(j, 0, t);
-    if (c < C) {
+    if (c0 < C) {
       Raw8<T> w;
       w.pack(v);
-      w.store(row + c);
+      w.store(row + c0);
     }
   } else {
+    T* const p = row + c0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = channel<false>(j, e, t);
-      if (c < C) row[c] = from_f32<T>(v[e]);
+    for (int e = 0; e < 8; ++e)
+      if (c0 + e * 32 < C) p[e * 32] = from_f32<T>(v[e]);
+  }
+}
+
+// Sums of N (1 or 3) values over a CTA of at most MAX_WARPS warps, the same in every thread and in a fixed order.
+// `buf` (N * 32 floats, cleared by clear_sums) is one of two areas used in turn, so one barrier per call is enough.
+// Three values share the rounds within a warp: after two of them a lane has the sum of only one value.
+template <int MAX_WARPS, int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
+  static_assert(N == 1 || N == 3, "");
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  auto add = [](float x, int o) { return x + __shfl_xor_sync(0xffffffffu, x, o); };
+  float z;
+  int mine = 0;
+  if (N == 1) {
+    z = add(add(v[0], 16), 8);
+  } else {
+    const bool a = lane & 16, b = lane & 8;  // lanes 0-7: the first, 16-23: the second, 8-15 and 24-31: the third
+    const float x = (a ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, a ? v[0] : v[1], 16), y = add(v[N - 1], 16);
+    z = (b ? y : x) + __shfl_xor_sync(0xffffffffu, b ? x : y, 8);
+    mine = b ? 2 : a ? 1 : 0;
+  }
+  z = add(add(add(z, 4), 2), 1);
+  if (warps == 1) {
+    if (N == 1) {
+      v[0] = z;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, z, i == 0 ? 0 : i == 1 ? 16 : 8);
     }
+    return;
+  }
+  if (N == 1 ? lane == 0 : (lane & 7) == 0 && lane < 24) buf[mine * 32 + (threadIdx.x >> 5)] = z;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {  // four warps' sums a lane
+    const float4 f = *reinterpret_cast<const float4*>(buf + i * 32 + (lane & (MAX_WARPS / 4 - 1)) * 4);
+    v[i] = (f.x + f.y) + (f.z + f.w);
+#pragma unroll
+    for (int o = MAX_WARPS / 8; o > 0; o >>= 1) v[i] = add(v[i], o);
   }
 }
-
-// The same in a loop that skips a thread's vectors behind the row (`absent`): filling them with zeros, load by load,
-// was a sixth of the backward's instructions.
-template <bool VEC>
-__device__ __forceinline__ bool absent(int j, int C) {
-  return VEC && channel<true>(j, 0, blockDim.x) >= C;
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void get8(const T* row, int j, int C, float (&v)[8]) {
-  if (VEC) {
-    Raw8<T> w;
-    w.load(row + channel<true>(j, 0, blockDim.x));
-    w.unpack(v);
-  } else {
-    load8<false>(row, j, C, v);
-  }
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void put8(T* row, int j, int C, const float (&v)[8]) {
-  if (VEC) {
-    Raw8<T> w;
-    w.pack(v);
-    w.store(row + channel<true>(j, 0, blockDim.x));
-  } else {
-    store8<false>(row, j, C, v);
-  }
-}
-
-// Sums of N values over the CTA's first t threads (which meet at barrier 1), the same in every thread and in
-// a fixed order.  `buf` is one of two areas of 32 * N floats used in turn, so one barrier per call is enough.
+// (The entries of warps that are not there; written before the first barrier of block_sums.)
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int t = blockDim.x) {
+__device__ __forceinline__ void clear_sums(float (&buf)[2][N]) {
+  const int i = static_cast<int>(threadIdx.x);
+  if (i < 32 && i >= static_cast<int>(blockDim.x >> 5))
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int warps = t >> 5;
-  if (warps == 1) return;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) buf[i * 32 + (threadIdx.x >> 5)] = v[i];
-  tcdev::named_barrier(static_cast<uint32_t>(t));
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = static_cast<int>(threadIdx.x & 31) < warps ? buf[i * 32 + (threadIdx.x & 31)] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int k = 0; k < 2 * N; k += 32) buf[k / N][k % N + i] = 0.f;
 }
 
 // The gate row of a row that only moves on: a 64-bit division costs as much as the rest of a row's
@@ -152,30 +153,31 @@ struct FwdArgs {
 
 template <typename T, int NV, bool VEC, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) block_norm_fwd_kernel(const FwdArgs a) {
-  __shared__ float sums[2][32];
+  __shared__ __align__(16) float sums[2][32];
+  clear_sums(sums);
   const int C = a.C;
   const float inv = 1.f / static_cast<float>(C);
   GateRow gate_row;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float r[NV][8];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load8<VEC>(static_cast<const T*>(a.residual) + row * C, j, C, r[j]);
+    for (int j = 0; j < NV; ++j) load8<VEC, NV>(static_cast<const T*>(a.residual) + row * C, j, C, r[j]);
     if (a.block) {
       float b[NV][8];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) load8<VEC>(static_cast<const T*>(a.block) + row * C, j, C, b[j]);
+      for (int j = 0; j < NV; ++j) load8<VEC, NV>(static_cast<const T*>(a.block) + row * C, j, C, b[j]);
       if (a.post) {
         float s[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[0] = fmaf(b[j][e], b[j][e], s[0]);
-        block_sums(s, sums[0]);
+        block_sums<MAX_THREADS / 32>(s, sums[0]);
         const float bs = rsqrtf(fmaf(s[0], inv, a.eps));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float w[8];
-          load8<VEC>(a.post, j, C, w);
+          load8<VEC, NV>(a.post, j, C, w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) b[j][e] = b[j][e] * bs * w[e];
         }
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_fwd_kernel(const FwdAr
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float g[8];
-          load8<VEC>(gr, j, C, g);
+          load8<VEC, NV>(gr, j, C, g);
 #pragma unroll
           for (int e = 0; e < 8; ++e) b[j][e] *= g[e];
         }
@@ -197,22 +199,22 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_fwd_kernel(const FwdAr
     }
     if (a.residual_out)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store8<VEC>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+      for (int j = 0; j < NV; ++j) store8<VEC, NV>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
     if (a.normed) {
       float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[0] = fmaf(r[j][e], r[j][e], s[0]);
-      block_sums(s, sums[1]);
+      block_sums<MAX_THREADS / 32>(s, sums[1]);
       const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[8];
-        load8<VEC>(a.pre, j, C, w);
+        load8<VEC, NV>(a.pre, j, C, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[j][e] = r[j][e] * rs * w[e];
-        store8<VEC>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
+        store8<VEC, NV>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
       }
     }
     if (!a.post || !a.normed) __syncthreads();  // with both, the reductions' areas alternate
@@ -236,7 +238,8 @@ struct BwdArgs {
 // its rows, else as the CTA's first (0: begun by an earlier CTA) or last (1) partial.
 template <typename T, int NV, bool VEC, bool SUMS_IN_REGS, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdArgs a) {
-  __shared__ float sums[2][3 * 32];
+  __shared__ __align__(16) float sums[2][3 * 32];
+  clear_sums(sums);
   const int C = a.C;
   const float inv = 1.f / static_cast<float>(C);
   const int64_t first = blockIdx.x * a.rows_per_cta, last = min(first + a.rows_per_cta, a.rows);
@@ -254,8 +257,8 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (part_pre) store8<VEC>(part_pre, j, C, zero);
-      if (part_post) store8<VEC>(part_post, j, C, zero);
+      if (part_pre) store8<VEC, NV>(part_pre, j, C, zero);
+      if (part_post) store8<VEC, NV>(part_post, j, C, zero);
     }
   }
   float* gate_to = nullptr;  // where the current gate row's sum goes
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
       if (SUMS_IN_REGS && gate_to) {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
-          store8<VEC>(gate_to, j, C, agate[j]);
+          store8<VEC, NV>(gate_to, j, C, agate[j]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) agate[j][e] = 0.f;
         }
@@ -278,20 +281,20 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
       else gate_to = a.d_gate + g * C;
       if (!SUMS_IN_REGS)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) store8<VEC>(gate_to, j, C, zero);
+        for (int j = 0; j < NV; ++j) store8<VEC, NV>(gate_to, j, C, zero);
     }
     float dr[NV][8], b[NV][8];
     float s[3] = {0.f, 0.f, 0.f};  // r'^2, u r', b^2
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (a.block) {
-        load8<VEC>(static_cast<const T*>(a.block) + row * C, j, C, b[j]);
+        load8<VEC, NV>(static_cast<const T*>(a.block) + row * C, j, C, b[j]);
         if (a.post)
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[2] = fmaf(b[j][e], b[j][e], s[2]);
       }
       if (a.d_out) {
-        load8<VEC>(static_cast<const T*>(a.d_out) + row * C, j, C, dr[j]);
+        load8<VEC, NV>(static_cast<const T*>(a.d_out) + row * C, j, C, dr[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dr[j][e] = 0.f;
@@ -301,23 +304,23 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
       float r[NV][8], dn[NV][8];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        load8<VEC>(static_cast<const T*>(a.residual_out) + row * C, j, C, r[j]);
-        load8<VEC>(static_cast<const T*>(a.d_normed) + row * C, j, C, dn[j]);
+        load8<VEC, NV>(static_cast<const T*>(a.residual_out) + row * C, j, C, r[j]);
+        load8<VEC, NV>(static_cast<const T*>(a.d_normed) + row * C, j, C, dn[j]);
         float w[8];
-        load8<VEC>(a.pre, j, C, w);
+        load8<VEC, NV>(a.pre, j, C, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           s[0] = fmaf(r[j][e], r[j][e], s[0]);
           s[1] = fmaf(dn[j][e] * w[e], r[j][e], s[1]);
         }
       }
-      block_sums(s, sums[0]);
+      block_sums<MAX_THREADS / 32>(s, sums[0]);
       const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
       const float m = s[1] * inv * rs * rs;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[8], add[8];
-        load8<VEC>(a.pre, j, C, w);
+        load8<VEC, NV>(a.pre, j, C, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           dr[j][e] = fmaf(rs, fmaf(dn[j][e], w[e], -r[j][e] * m), dr[j][e]);
@@ -329,19 +332,19 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
             for (int e = 0; e < 8; ++e) apre[SUMS_IN_REGS ? j : 0][e] += add[e];
           } else {
             float t[8];
-            load8<VEC>(part_pre, j, C, t);
+            load8<VEC, NV>(part_pre, j, C, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] += add[e];
-            store8<VEC>(part_pre, j, C, t);
+            store8<VEC, NV>(part_pre, j, C, t);
           }
         }
       }
     } else if (a.post) {
-      block_sums(s, sums[0]);
+      block_sums<MAX_THREADS / 32>(s, sums[0]);
     }
     if (a.d_residual)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store8<VEC>(static_cast<T*>(a.d_residual) + row * C, j, C, dr[j]);
+      for (int j = 0; j < NV; ++j) store8<VEC, NV>(static_cast<T*>(a.d_residual) + row * C, j, C, dr[j]);
     if (a.block) {
       const float bs = a.post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.f;
       float c[1] = {0.f};
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
       for (int j = 0; j < NV; ++j) {
         float w[8];
         if (a.post) {
-          load8<VEC>(a.post, j, C, w);
+          load8<VEC, NV>(a.post, j, C, w);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = 1.f;
@@ -363,15 +366,15 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
             for (int e = 0; e < 8; ++e) agate[SUMS_IN_REGS ? j : 0][e] += add[e];
           } else {
             float t[8];
-            load8<VEC>(gate_to, j, C, t);
+            load8<VEC, NV>(gate_to, j, C, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] += add[e];
-            store8<VEC>(gate_to, j, C, t);
+            store8<VEC, NV>(gate_to, j, C, t);
           }
         }
         float g[8];
         if (g_row) {
-          load8<VEC>(g_row, j, C, g);
+          load8<VEC, NV>(g_row, j, C, g);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] = 1.f;
@@ -387,10 +390,10 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
             for (int e = 0; e < 8; ++e) apost[SUMS_IN_REGS ? j : 0][e] += add[e];
           } else {
             float t[8];
-            load8<VEC>(part_post, j, C, t);
+            load8<VEC, NV>(part_post, j, C, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] += add[e];
-            store8<VEC>(part_post, j, C, t);
+            store8<VEC, NV>(part_post, j, C, t);
           }
         }
 #pragma unroll
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
       }
       float m = 0.f;
       if (a.post) {
-        block_sums(c, sums[1]);
+        block_sums<MAX_THREADS / 32>(c, sums[1]);
         m = c[0] * inv * bs * bs;
       }
       if (a.d_block)
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) dr[j][e] = bs * (dr[j][e] - b[j][e] * m);
-          store8<VEC>(static_cast<T*>(a.d_block) + row * C, j, C, dr[j]);
+          store8<VEC, NV>(static_cast<T*>(a.d_block) + row * C, j, C, dr[j]);
         }
     }
     if (!a.post) __syncthreads();  // with both reductions, their areas alternate
@@ -417,9 +420,9 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
   if (SUMS_IN_REGS) {
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      if (part_pre) store8<VEC>(part_pre, j, C, apre[j]);
-      if (part_post) store8<VEC>(part_post, j, C, apost[j]);
-      if (gate_to) store8<VEC>(gate_to, j, C, agate[j]);
+      if (part_pre) store8<VEC, NV>(part_pre, j, C, apre[j]);
+      if (part_post) store8<VEC, NV>(part_post, j, C, apost[j]);
+      if (gate_to) store8<VEC, NV>(gate_to, j, C, agate[j]);
     }
   }
 }
@@ -510,6 +513,63 @@ __device__ __forceinline__ void ring_init(uint64_t* full, int stages) {
   __syncthreads();
 }
 
+// Loads and stores of rows in a loop that skips a thread's vectors behind the row (`absent`: filling them with zeros,
+// load by load, was a sixth of the backward's instructions); ALL: the thread's channels are all there.
+template <bool VEC>
+__device__ __forceinline__ bool absent(int j, int C) {
+  return VEC && channel<true, kRingNv>(j, 0) >= C;
+}
+template <bool VEC, bool ALL, typename T>
+__device__ __forceinline__ void get8(const T* row, int j, int C, float (&v)[8]) {
+  const T* const p = row + channel<VEC, kRingNv>(j, 0);
+  if (VEC) {
+    Raw8<T> w;
+    w.load(p);
+    w.unpack(v);
+  } else if (ALL) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(p[e * 32]);
+  } else {
+    load8<false, kRingNv>(row, j, C, v);
+  }
+}
+template <bool VEC, bool ALL, typename T>
+__device__ __forceinline__ void put8(T* row, int j, int C, const float (&v)[8]) {
+  T* const p = row + channel<VEC, kRingNv>(j, 0);
+  if (VEC) {
+    Raw8<T> w;
+    w.pack(v);
+    w.store(p);
+  } else if (ALL) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e * 32] = from_f32<T>(v[e]);
+  } else {
+    store8<false, kRingNv>(row, j, C, v);
+  }
+}
+// The same as pairs, for the packed arithmetic.
+template <bool VEC, bool ALL, typename T>
+__device__ __forceinline__ void get4x2(const T* row, int j, int C, uint64_t (&v)[4]) {
+  float f[8];
+  get8<VEC, ALL>(row, j, C, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+template <bool VEC, bool ALL, typename T>
+__device__ __forceinline__ void put4x2(T* row, int j, int C, const uint64_t (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = half_of(v[i / 2], i & 1);
+  put8<VEC, ALL>(row, j, C, f);
+}
+__device__ __forceinline__ float both(uint64_t v) { return half_of(v, 0) + half_of(v, 1); }
+// f(std::true_type) for threads whose channels are all there, else f(std::false_type); the same for a warp.
+template <bool VEC, typename F>
+__device__ __forceinline__ void with_channels(bool all, F&& f) {
+  if (VEC || all) f(std::true_type{});
+  else f(std::false_type{});
+}
+
 // Weights of a thread's channels in shared memory, read and written by that thread alone (so without barriers):
 // vector j's eight as two float4, side by side over the threads.
 struct OwnWeights {
@@ -518,10 +578,10 @@ struct OwnWeights {
     at[(2 * j) * blockDim.x + threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
     at[(2 * j + 1) * blockDim.x + threadIdx.x] = make_float4(w[4], w[5], w[6], w[7]);
   }
-  __device__ __forceinline__ void get(int j, float (&w)[8]) const {
+  __device__ __forceinline__ void get(int j, uint64_t (&w)[4]) const {
     const float4 a = at[(2 * j) * blockDim.x + threadIdx.x], b = at[(2 * j + 1) * blockDim.x + threadIdx.x];
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    w[0] = pair(a.x, a.y); w[1] = pair(a.z, a.w);
+    w[2] = pair(b.x, b.y); w[3] = pair(b.z, b.w);
   }
 };
 // Two sets of them lie in front of the ring.
@@ -535,8 +595,8 @@ __device__ __forceinline__ void put_gate_post(OwnWeights W, float alpha, const T
     float g[8], w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = w[e] = 1.f;
-    if (gate) load8<VEC>(gate, j, C, g);
-    if (post) load8<VEC>(post, j, C, w);
+    if (gate) load8<VEC, kRingNv>(gate, j, C, g);
+    if (post) load8<VEC, kRingNv>(post, j, C, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] *= alpha * g[e];
     W.put(j, w);
@@ -546,9 +606,11 @@ __device__ __forceinline__ void put_gate_post(OwnWeights W, float alpha, const T
 template <typename T, bool VEC, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block_norm_fwd_ring_kernel(const FwdArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[2][32];
+  __shared__ __align__(16) float sums[2][32];
   __shared__ uint64_t full[kMaxRing];
+  clear_sums(sums);
   constexpr int NV = kRingNv;
+  const bool all = whole<NV>(a.C);
   const int C = a.C, stage_bytes = 2 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
   OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
   uint8_t* const ring = smem + 2 * own;
@@ -563,9 +625,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
   if (a.pre)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
       float w[8];
-      get8<VEC>(a.pre, j, C, w);
+      load8<VEC, NV>(a.pre, j, C, w);
       pre.put(j, w);
     }
   if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
@@ -578,18 +639,22 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
     ring_wait(&full[s], parity);
     uint8_t* const stage = ring + s * stage_bytes;
     const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const b_row = ring_at<T, VEC>(stage, 1, src[1], C, row);
-    float r[NV][8], b[NV][8], q[1] = {0.f};
+    uint64_t r[NV][4], b[NV][4], qq = 0;
+    with_channels<VEC>(all, [&](auto is_all) {
+      constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
-      get8<VEC>(r_row, j, C, r[j]);
-      if (a.block) {
-        get8<VEC>(b_row, j, C, b[j]);
+      for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
+        get4x2<VEC, ALL>(r_row, j, C, r[j]);
+        if (a.block) {
+          get4x2<VEC, ALL>(b_row, j, C, b[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] = fmaf(b[j][e], b[j][e], q[0]);
+          for (int i = 0; i < 4; ++i) qq = fma2(b[j][i], b[j][i], qq);
+        }
       }
-    }
-    if (a.post) block_sums(q, sums[0]);
+    });
+    float q[1] = {both(qq)};
+    if (a.post) block_sums<MAX_THREADS / 32>(q, sums[0]);
     else __syncthreads();
     if (threadIdx.x < 32 && row + stages * step < a.rows && tcdev::elect_one())  // everyone has read this stage
       ring_request<T, VEC>(&full[s], stage, src, C, row + stages * step, a.rows);
@@ -600,38 +665,44 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
     }
     if (a.block) {
       const float bs = a.post ? rsqrtf(fmaf(q[0], inv, a.eps)) : 1.f;
+      const uint64_t bs2 = pair(bs, bs);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (absent<VEC>(j, C)) continue;
-        float w[8];
+        uint64_t w[4];
         gate_post.get(j, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] = fmaf(b[j][e] * bs, w[e], r[j][e]);
+        for (int i = 0; i < 4; ++i) r[j][i] = fma2(mul2(b[j][i], bs2), w[i], r[j][i]);
       }
     }
-    if (a.residual_out)
+    uint64_t tt = 0;
+    with_channels<VEC>(all, [&](auto is_all) {
+      constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (!absent<VEC>(j, C)) put8<VEC>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+      for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
+        if (a.residual_out) put4x2<VEC, ALL>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tt = fma2(r[j][i], r[j][i], tt);
+      }
+    });
     if (a.normed) {
-      float t[1] = {0.f};
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[0] = fmaf(r[j][e], r[j][e], t[0]);
-      }
-      block_sums(t, sums[1]);
+      float t[1] = {both(tt)};
+      block_sums<MAX_THREADS / 32>(t, sums[1]);
       const float rs = rsqrtf(fmaf(t[0], inv, a.eps));
+      const uint64_t rs2 = pair(rs, rs);
+      with_channels<VEC>(all, [&](auto is_all) {
+        constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
-        float w[8];
-        pre.get(j, w);
+        for (int j = 0; j < NV; ++j) {
+          if (absent<VEC>(j, C)) continue;
+          uint64_t w[4];
+          pre.get(j, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] = r[j][e] * rs * w[e];
-        put8<VEC>(static_cast<T*>(a.normed) + row * C, j, C, r[j]);
-      }
+          for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(r[j][i], rs2), w[i]);
+          put4x2<VEC, ALL>(static_cast<T*>(a.normed) + row * C, j, C, w);
+        }
+      });
     }
     if (a.post && !a.normed) __syncthreads();  // (otherwise there are two barriers a row, and the areas alternate)
   }
@@ -645,9 +716,11 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
 template <typename T, bool VEC, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block_norm_bwd_ring_kernel(const BwdArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[2][3 * 32];
+  __shared__ __align__(16) float sums[2][3 * 32];
   __shared__ uint64_t full[kMaxRing];
+  clear_sums(sums);
   constexpr int NV = kRingNv;
+  const bool all = whole<NV>(a.C);
   const int C = a.C, stage_bytes = 4 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
   OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
   uint8_t* const ring = smem + 2 * own;
@@ -664,17 +737,16 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   if (a.pre)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
       float w[8];
-      get8<VEC>(a.pre, j, C, w);
+      load8<VEC, NV>(a.pre, j, C, w);
       pre.put(j, w);
     }
   if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
-  float apre[NV][8], sum[NV][8];
+  uint64_t apre[NV][4], sum[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) apre[j][e] = sum[j][e] = 0.f;
+    for (int i = 0; i < 4; ++i) apre[j][i] = sum[j][i] = 0;
   // the sum of the rows of one gate row goes where it belongs
   float* gate_to = nullptr;
   GateRow gate_row;
@@ -683,27 +755,28 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   auto flush = [&]() {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
-      float w[8];
-      if (gate_to) {
-        if (a.post) get8<VEC>(a.post, j, C, w);
+      float f[8], w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = a.post ? w[e] * sum[j][e] : sum[j][e];
-        put8<VEC>(gate_to, j, C, w);
+      for (int e = 0; e < 8; ++e) f[e] = half_of(sum[j][e / 2], e & 1);
+      if (gate_to) {
+        if (a.post) load8<VEC, NV>(a.post, j, C, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = a.post ? w[e] * f[e] : f[e];
+        store8<VEC, NV>(gate_to, j, C, w);
       }
       if (a.sum_post) {
         float t[8];
-        if (g_row) get8<VEC>(g_row, j, C, w);
-        if (flushed) get8<VEC>(a.sum_post + cta * C, j, C, t);
+        if (g_row) load8<VEC, NV>(g_row, j, C, w);
+        if (flushed) load8<VEC, NV>(a.sum_post + cta * C, j, C, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float add = g_row ? w[e] * sum[j][e] : sum[j][e];
+          const float add = g_row ? w[e] * f[e] : f[e];
           t[e] = flushed ? t[e] + add : add;
         }
-        put8<VEC>(a.sum_post + cta * C, j, C, t);
+        store8<VEC, NV>(a.sum_post + cta * C, j, C, t);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[j][e] = 0.f;
+      for (int i = 0; i < 4; ++i) sum[j][i] = 0;
     }
     flushed = true;
   };
@@ -725,29 +798,33 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     uint8_t* const stage = ring + s * stage_bytes;
     const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const dn_row = ring_at<T, VEC>(stage, 1, src[1], C, row),
             *const do_row = ring_at<T, VEC>(stage, 2, src[2], C, row), *const b_row = ring_at<T, VEC>(stage, 3, src[3], C, row);
-    float t[3] = {0.f, 0.f, 0.f};  // r'^2, u r', b^2
+    uint64_t tr = 0, tu = 0, tb = 0;  // r'^2, u r', b^2
+    with_channels<VEC>(all, [&](auto is_all) {
+      constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
-      if (a.d_normed) {
-        float r[8], dn[8], w[8];
-        get8<VEC>(r_row, j, C, r);
-        get8<VEC>(dn_row, j, C, dn);
-        pre.get(j, w);
+      for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
+        if (a.d_normed) {
+          uint64_t r[4], dn[4], w[4];
+          get4x2<VEC, ALL>(r_row, j, C, r);
+          get4x2<VEC, ALL>(dn_row, j, C, dn);
+          pre.get(j, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          t[0] = fmaf(r[e], r[e], t[0]);
-          t[1] = fmaf(dn[e] * w[e], r[e], t[1]);
+          for (int i = 0; i < 4; ++i) {
+            tr = fma2(r[i], r[i], tr);
+            tu = fma2(mul2(dn[i], w[i]), r[i], tu);
+          }
+        }
+        if (a.post) {
+          uint64_t b[4];
+          get4x2<VEC, ALL>(b_row, j, C, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tb = fma2(b[i], b[i], tb);
         }
       }
-      if (a.post) {
-        float b[8];
-        get8<VEC>(b_row, j, C, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[2] = fmaf(b[e], b[e], t[2]);
-      }
-    }
-    block_sums(t, sums[0]);
+    });
+    float t[3] = {both(tr), both(tu), both(tb)};
+    block_sums<MAX_THREADS / 32>(t, sums[0]);
     const int64_t next = row - 1 + stages;
     if (threadIdx.x < 32 && row > first && next < last && tcdev::elect_one()) {
       const int sp = s == 0 ? stages - 1 : s - 1;
@@ -756,57 +833,67 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     __syncwarp();
     const float rs = rsqrtf(fmaf(t[0], inv, a.eps)), m = t[1] * inv * rs * rs;
     const float bs = a.post ? rsqrtf(fmaf(t[2], inv, a.eps)) : 1.f, abs_ = a.alpha * bs;
-    float c[1] = {0.f}, v[NV][8];
+    const uint64_t rs2 = pair(rs, rs), m2 = pair(-m, -m), abs2 = pair(abs_, abs_);
+    uint64_t cc = 0, v[NV][4];
+    with_channels<VEC>(all, [&](auto is_all) {
+      constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (absent<VEC>(j, C)) continue;
-      float dr[8], w[8];
-      if (a.d_out) {
-        get8<VEC>(do_row, j, C, dr);
-      } else {
+      for (int j = 0; j < NV; ++j) {
+        if (absent<VEC>(j, C)) continue;
+        uint64_t dr[4], w[4];
+        if (a.d_out) {
+          get4x2<VEC, ALL>(do_row, j, C, dr);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dr[e] = 0.f;
-      }
-      if (a.d_normed) {
-        float r[8], dn[8];
-        get8<VEC>(r_row, j, C, r);
-        get8<VEC>(dn_row, j, C, dn);
-        pre.get(j, w);
+          for (int i = 0; i < 4; ++i) dr[i] = 0;
+        }
+        if (a.d_normed) {
+          uint64_t r[4], dn[4];
+          get4x2<VEC, ALL>(r_row, j, C, r);
+          get4x2<VEC, ALL>(dn_row, j, C, dn);
+          pre.get(j, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dr[e] = fmaf(rs, fmaf(dn[e], w[e], -r[e] * m), dr[e]);
-          apre[j][e] = fmaf(dn[e], r[e] * rs, apre[j][e]);
+          for (int i = 0; i < 4; ++i) {
+            dr[i] = fma2(rs2, fma2(dn[i], w[i], mul2(r[i], m2)), dr[i]);
+            apre[j][i] = fma2(dn[i], mul2(r[i], rs2), apre[j][i]);
+          }
+        }
+        if (a.d_residual) put4x2<VEC, ALL>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
+        if (a.block) {
+          uint64_t b[4];
+          get4x2<VEC, ALL>(b_row, j, C, b);
+          gate_post.get(j, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum[j][i] = fma2(dr[i], mul2(b[i], abs2), sum[j][i]);
+            v[j][i] = mul2(dr[i], w[i]);
+            cc = fma2(v[j][i], b[i], cc);
+          }
         }
       }
-      if (a.d_residual) put8<VEC>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
-      if (a.block) {
-        float b[8];
-        get8<VEC>(b_row, j, C, b);
-        gate_post.get(j, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum[j][e] = fmaf(dr[e], b[e] * abs_, sum[j][e]);
-          v[j][e] = dr[e] * w[e];
-          c[0] = fmaf(v[j][e], b[e], c[0]);
-        }
-      }
-    }
+    });
     if (a.block) {
       float mb = 0.f;
       if (a.post) {
-        block_sums(c, sums[1]);
+        float c[1] = {both(cc)};
+        block_sums<MAX_THREADS / 32>(c, sums[1]);
         mb = c[0] * inv * bs * bs;
       }
-      if (a.d_block)
+      if (a.d_block) {
+        const uint64_t bs2 = pair(bs, bs), mb2 = pair(-mb, -mb);
+        with_channels<VEC>(all, [&](auto is_all) {
+          constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          if (absent<VEC>(j, C)) continue;
-          float b[8];
-          get8<VEC>(b_row, j, C, b);
+          for (int j = 0; j < NV; ++j) {
+            if (absent<VEC>(j, C)) continue;
+            uint64_t b[4];
+            get4x2<VEC, ALL>(b_row, j, C, b);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] = bs * (v[j][e] - b[e] * mb);
-          put8<VEC>(static_cast<T*>(a.d_block) + row * C, j, C, b);
-        }
+            for (int i = 0; i < 4; ++i) b[i] = mul2(bs2, fma2(b[i], mb2, v[j][i]));
+            put4x2<VEC, ALL>(static_cast<T*>(a.d_block) + row * C, j, C, b);
+          }
+        });
+      }
     }
     if (!a.block || !a.post) __syncthreads();  // with both reductions, their areas alternate
     if (++s == stages) {
@@ -815,9 +902,14 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     }
   }
   flush();
+  if (a.sum_pre)
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (a.sum_pre && !absent<VEC>(j, C)) put8<VEC>(a.sum_pre + cta * C, j, C, apre[j]);
+    for (int j = 0; j < NV; ++j) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = half_of(apre[j][e / 2], e & 1);
+      store8<VEC, NV>(a.sum_pre + cta * C, j, C, f);
+    }
 }
 
 struct SumArgs {

@@ -41,6 +41,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "host_util.cuh"
 #include "quant_fc.cuh"
 #include "tc_device.cuh"
@@ -147,20 +148,6 @@ __device__ __forceinline__ void ld_wait(uint32_t (&v)[16]) {
 }
 
 // Two 32-bit registers as one of 64 bits, its halves as fp32, and the packed multiply-add on such pairs.
-__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float half_of(uint64_t p, int high) {
-  return __uint_as_float(static_cast<uint32_t>(high ? p >> 32 : p));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Barriers by their shared-memory address: what a single thread does between two MMAs is on the
 // critical path, instruction by instruction.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -567,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              acc[c * 8 + j] = fma_f32x2(sc2, pair_u32(v[c & 1][2 * j], v[c & 1][2 * j + 1]), acc[c * 8 + j]);
+              acc[c * 8 + j] = fma2(sc2, pair_u32(v[c & 1][2 * j], v[c & 1][2 * j + 1]), acc[c * 8 + j]);
           }
         turn ^= 1u;
         if (turn == 0) phase ^= 1u;

@@ -31,6 +31,7 @@
 
 #include "common.cuh"
 #include "dtype.cuh"
+#include "f32x2.cuh"
 #include "host_util.cuh"
 #include "tc_device.cuh"
 
@@ -122,28 +123,6 @@ __device__ __forceinline__ Stat join_lanes(Stat st, float c) {
     st = join(st, b, c);
   }
   return st;
-}
-
-// Two fp32 numbers in a 64-bit register, for the packed instructions.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // A thread's running statistics: those of Stat with separate sums for even and odd elements.
