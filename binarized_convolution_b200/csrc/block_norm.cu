@@ -29,7 +29,8 @@ namespace bconv {
 namespace {
 
 constexpr int kMaxWidth = 32768;
-constexpr int kSumRows = 16;  // partial rows a column of the final sums is split over
+constexpr int kSumRows = 16;   // threads that a column of the final sums is split over
+constexpr int kSumChains = 8;  // sums of a thread (short chains: 2368 partial rows in 21 + 3 + 16 additions)
 
 // Where the 8 * j + e-th of a thread's NV * 8 channels of a row is: with VEC, 8 consecutive channels per j (16-byte
 // accesses; C % 8 == 0 and every row 16-byte aligned), else one channel per access, a warp's side by side and
@@ -108,6 +109,7 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, z, i == 0 ? 0 : i == 1 ? 16 : 8);
     }
+    __syncwarp();
     return;
   }
   if (N == 1 ? lane == 0 : (lane & 7) == 0 && lane < 24) buf[mine * 32 + (threadIdx.x >> 5)] = z;
@@ -438,9 +440,9 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_bwd_kernel(const BwdAr
 // the same offset from a 16-byte boundary as in memory.
 
 constexpr int kRingLow = 256, kRingHigh = 8192;  // widths served
-constexpr int kRingNv = 2;                       // 8-channel vectors of a thread
 constexpr int kRingBytes = 216 * 1024;           // of an SM
 constexpr int kMaxRing = 4;
+constexpr int kBwdNv = 2;                        // 8-channel vectors of a thread (one: 81 us for 4096 x 4096, not 58)
 
 // (Copies that were issued always arrive; the limit of a second only keeps a wait from being endless.)
 __device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity) {
@@ -515,13 +517,13 @@ __device__ __forceinline__ void ring_init(uint64_t* full, int stages) {
 
 // Loads and stores of rows in a loop that skips a thread's vectors behind the row (`absent`: filling them with zeros,
 // load by load, was a sixth of the backward's instructions); ALL: the thread's channels are all there.
-template <bool VEC>
+template <bool VEC, int NV>
 __device__ __forceinline__ bool absent(int j, int C) {
-  return VEC && channel<true, kRingNv>(j, 0) >= C;
+  return VEC && channel<true, NV>(j, 0) >= C;
 }
-template <bool VEC, bool ALL, typename T>
+template <bool VEC, bool ALL, int NV, typename T>
 __device__ __forceinline__ void get8(const T* row, int j, int C, float (&v)[8]) {
-  const T* const p = row + channel<VEC, kRingNv>(j, 0);
+  const T* const p = row + channel<VEC, NV>(j, 0);
   if (VEC) {
     Raw8<T> w;
     w.load(p);
@@ -530,12 +532,12 @@ __device__ __forceinline__ void get8(const T* row, int j, int C, float (&v)[8]) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = to_f32(p[e * 32]);
   } else {
-    load8<false, kRingNv>(row, j, C, v);
+    load8<false, NV>(row, j, C, v);
   }
 }
-template <bool VEC, bool ALL, typename T>
+template <bool VEC, bool ALL, int NV, typename T>
 __device__ __forceinline__ void put8(T* row, int j, int C, const float (&v)[8]) {
-  T* const p = row + channel<VEC, kRingNv>(j, 0);
+  T* const p = row + channel<VEC, NV>(j, 0);
   if (VEC) {
     Raw8<T> w;
     w.pack(v);
@@ -544,23 +546,23 @@ __device__ __forceinline__ void put8(T* row, int j, int C, const float (&v)[8]) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e * 32] = from_f32<T>(v[e]);
   } else {
-    store8<false, kRingNv>(row, j, C, v);
+    store8<false, NV>(row, j, C, v);
   }
 }
 // The same as pairs, for the packed arithmetic.
-template <bool VEC, bool ALL, typename T>
+template <bool VEC, bool ALL, int NV, typename T>
 __device__ __forceinline__ void get4x2(const T* row, int j, int C, uint64_t (&v)[4]) {
   float f[8];
-  get8<VEC, ALL>(row, j, C, f);
+  get8<VEC, ALL, NV>(row, j, C, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
 }
-template <bool VEC, bool ALL, typename T>
+template <bool VEC, bool ALL, int NV, typename T>
 __device__ __forceinline__ void put4x2(T* row, int j, int C, const uint64_t (&v)[4]) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = half_of(v[i / 2], i & 1);
-  put8<VEC, ALL>(row, j, C, f);
+  put8<VEC, ALL, NV>(row, j, C, f);
 }
 __device__ __forceinline__ float both(uint64_t v) { return half_of(v, 0) + half_of(v, 1); }
 // f(std::true_type) for threads whose channels are all there, else f(std::false_type); the same for a warp.
@@ -585,33 +587,35 @@ struct OwnWeights {
   }
 };
 // Two sets of them lie in front of the ring.
-__host__ __device__ constexpr int own_weight_bytes(int threads) { return threads * kRingNv * 8 * 4; }
+__host__ __device__ constexpr int own_weight_bytes(int threads, int nv) { return threads * nv * 8 * 4; }
 
 // alpha * gate * post of this thread's channels (either may be NULL: 1)
-template <typename T, bool VEC>
+template <typename T, bool VEC, int NV>
 __device__ __forceinline__ void put_gate_post(OwnWeights W, float alpha, const T* gate, const float* post, int C) {
 #pragma unroll
-  for (int j = 0; j < kRingNv; ++j) {
+  for (int j = 0; j < NV; ++j) {
     float g[8], w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = w[e] = 1.f;
-    if (gate) load8<VEC, kRingNv>(gate, j, C, g);
-    if (post) load8<VEC, kRingNv>(post, j, C, w);
+    if (gate) load8<VEC, NV>(gate, j, C, g);
+    if (post) load8<VEC, NV>(post, j, C, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] *= alpha * g[e];
     W.put(j, w);
   }
 }
 
-template <typename T, bool VEC, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block_norm_fwd_ring_kernel(const FwdArgs a, int stages) {
+// NV: 8-channel vectors of a thread.  Two, or one for fp32, whose rows leave room for only half as many CTAs (4096 x 4096:
+// 46.4 us against 50.1, 8000 x 2001: 50.3 against 60.6; bf16 30.1 against 28.5).
+template <typename T, bool VEC, int NV, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : NV == 1 && MAX_THREADS == 512 ? 2 : 1)
+    block_norm_fwd_ring_kernel(const FwdArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float sums[2][32];
   __shared__ uint64_t full[kMaxRing];
   clear_sums(sums);
-  constexpr int NV = kRingNv;
   const bool all = whole<NV>(a.C);
-  const int C = a.C, stage_bytes = 2 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
+  const int C = a.C, stage_bytes = 2 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x, NV);
   OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
   uint8_t* const ring = smem + 2 * own;
   const float inv = 1.f / static_cast<float>(C);
@@ -629,13 +633,13 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
       load8<VEC, NV>(a.pre, j, C, w);
       pre.put(j, w);
     }
-  if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
+  if (!a.gate) put_gate_post<T, VEC, NV>(gate_post, a.alpha, nullptr, a.post, C);
   int s = 0;
   uint32_t parity = 0;
   GateRow gate_row;
   for (int64_t row = blockIdx.x; row < a.rows; row += step) {
     if (a.gate && row >= gate_row.end)
-      put_gate_post<T, VEC>(gate_post, a.alpha, static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C, a.post, C);
+      put_gate_post<T, VEC, NV>(gate_post, a.alpha, static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C, a.post, C);
     ring_wait(&full[s], parity);
     uint8_t* const stage = ring + s * stage_bytes;
     const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const b_row = ring_at<T, VEC>(stage, 1, src[1], C, row);
@@ -644,10 +648,10 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
       constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
-        get4x2<VEC, ALL>(r_row, j, C, r[j]);
+        if (absent<VEC, NV>(j, C)) continue;
+        get4x2<VEC, ALL, NV>(r_row, j, C, r[j]);
         if (a.block) {
-          get4x2<VEC, ALL>(b_row, j, C, b[j]);
+          get4x2<VEC, ALL, NV>(b_row, j, C, b[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) qq = fma2(b[j][i], b[j][i], qq);
         }
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
       const uint64_t bs2 = pair(bs, bs);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
+        if (absent<VEC, NV>(j, C)) continue;
         uint64_t w[4];
         gate_post.get(j, w);
 #pragma unroll
@@ -680,8 +684,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
       constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
-        if (a.residual_out) put4x2<VEC, ALL>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
+        if (absent<VEC, NV>(j, C)) continue;
+        if (a.residual_out) put4x2<VEC, ALL, NV>(static_cast<T*>(a.residual_out) + row * C, j, C, r[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tt = fma2(r[j][i], r[j][i], tt);
       }
@@ -695,12 +699,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
         constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          if (absent<VEC>(j, C)) continue;
+          if (absent<VEC, NV>(j, C)) continue;
           uint64_t w[4];
           pre.get(j, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(r[j][i], rs2), w[i]);
-          put4x2<VEC, ALL>(static_cast<T*>(a.normed) + row * C, j, C, w);
+          put4x2<VEC, ALL, NV>(static_cast<T*>(a.normed) + row * C, j, C, w);
         }
       });
     }
@@ -712,16 +716,17 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : 1) block
 //     S = sum_rows a dR b bs     d_gate = w_post S     d_post_weight = g S
 // times what does not change, so registers hold S, and d_post_weight's partial sums (in memory) are brought up
 // to date with the gate.  A row's stage is requested again in the next row, behind the barrier that shows that
-// everyone is done with it.
+// everyone is done with it (all but the block's row already behind the row's second sum: 4096 x 4096 bf16 58.9 us
+// against 58.5, fp32 85.5 against 88.1).
 template <typename T, bool VEC, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block_norm_bwd_ring_kernel(const BwdArgs a, int stages) {
+  constexpr int NV = kBwdNv;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float sums[2][3 * 32];
   __shared__ uint64_t full[kMaxRing];
   clear_sums(sums);
-  constexpr int NV = kRingNv;
   const bool all = whole<NV>(a.C);
-  const int C = a.C, stage_bytes = 4 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x);
+  const int C = a.C, stage_bytes = 4 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x, NV);
   OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
   uint8_t* const ring = smem + 2 * own;
   const float inv = 1.f / static_cast<float>(C);
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       load8<VEC, NV>(a.pre, j, C, w);
       pre.put(j, w);
     }
-  if (!a.gate) put_gate_post<T, VEC>(gate_post, a.alpha, nullptr, a.post, C);
+  if (!a.gate) put_gate_post<T, VEC, NV>(gate_post, a.alpha, nullptr, a.post, C);
   uint64_t apre[NV][4], sum[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -787,7 +792,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       if (g_row) flush();
       const int64_t g = gate_row.of(row, a.per_gate), begin = g * a.per_gate;
       g_row = static_cast<const T*>(a.gate) + g * C;
-      put_gate_post<T, VEC>(gate_post, a.alpha, g_row, a.post, C);
+      put_gate_post<T, VEC, NV>(gate_post, a.alpha, g_row, a.post, C);
       if (a.sum_gate) {
         if (begin < first) gate_to = a.sum_gate + (cta * 2) * C;
         else if (min(gate_row.end, a.rows) > last) gate_to = a.sum_gate + (cta * 2 + 1) * C;
@@ -803,11 +808,11 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
+        if (absent<VEC, NV>(j, C)) continue;
         if (a.d_normed) {
           uint64_t r[4], dn[4], w[4];
-          get4x2<VEC, ALL>(r_row, j, C, r);
-          get4x2<VEC, ALL>(dn_row, j, C, dn);
+          get4x2<VEC, ALL, NV>(r_row, j, C, r);
+          get4x2<VEC, ALL, NV>(dn_row, j, C, dn);
           pre.get(j, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -817,7 +822,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
         }
         if (a.post) {
           uint64_t b[4];
-          get4x2<VEC, ALL>(b_row, j, C, b);
+          get4x2<VEC, ALL, NV>(b_row, j, C, b);
 #pragma unroll
           for (int i = 0; i < 4; ++i) tb = fma2(b[i], b[i], tb);
         }
@@ -839,18 +844,18 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (absent<VEC>(j, C)) continue;
+        if (absent<VEC, NV>(j, C)) continue;
         uint64_t dr[4], w[4];
         if (a.d_out) {
-          get4x2<VEC, ALL>(do_row, j, C, dr);
+          get4x2<VEC, ALL, NV>(do_row, j, C, dr);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) dr[i] = 0;
         }
         if (a.d_normed) {
           uint64_t r[4], dn[4];
-          get4x2<VEC, ALL>(r_row, j, C, r);
-          get4x2<VEC, ALL>(dn_row, j, C, dn);
+          get4x2<VEC, ALL, NV>(r_row, j, C, r);
+          get4x2<VEC, ALL, NV>(dn_row, j, C, dn);
           pre.get(j, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -858,10 +863,10 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
             apre[j][i] = fma2(dn[i], mul2(r[i], rs2), apre[j][i]);
           }
         }
-        if (a.d_residual) put4x2<VEC, ALL>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
+        if (a.d_residual) put4x2<VEC, ALL, NV>(static_cast<T*>(a.d_residual) + row * C, j, C, dr);
         if (a.block) {
           uint64_t b[4];
-          get4x2<VEC, ALL>(b_row, j, C, b);
+          get4x2<VEC, ALL, NV>(b_row, j, C, b);
           gate_post.get(j, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -885,12 +890,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
           constexpr bool ALL = decltype(is_all)::value;
 #pragma unroll
           for (int j = 0; j < NV; ++j) {
-            if (absent<VEC>(j, C)) continue;
+            if (absent<VEC, NV>(j, C)) continue;
             uint64_t b[4];
-            get4x2<VEC, ALL>(b_row, j, C, b);
+            get4x2<VEC, ALL, NV>(b_row, j, C, b);
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = mul2(bs2, fma2(b[i], mb2, v[j][i]));
-            put4x2<VEC, ALL>(static_cast<T*>(a.d_block) + row * C, j, C, b);
+            put4x2<VEC, ALL, NV>(static_cast<T*>(a.d_block) + row * C, j, C, b);
           }
         });
       }
@@ -901,6 +906,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
       parity ^= 1u;
     }
   }
+  allow_next_grid();
   flush();
   if (a.sum_pre)
 #pragma unroll
@@ -924,6 +930,7 @@ struct SumArgs {
 // found it begun and is the first to do so (1 + i).
 __global__ void block_norm_sum_kernel(const SumArgs a) {
   __shared__ float part[kSumRows][33];
+  wait_prior_grid();
   const int c = blockIdx.x * 32 + threadIdx.x, y = blockIdx.y;
   const float* from = nullptr;  // row of partial `from_first`
   float* to = nullptr;
@@ -954,9 +961,25 @@ __global__ void block_norm_sum_kernel(const SumArgs a) {
   if (!to) return;
   float s = 0.f;
   if (c < a.C) {
-    if (extra && threadIdx.y == 0) s = extra[c];
-#pragma unroll 8
-    for (int64_t i = threadIdx.y; i < n; i += kSumRows) s += from[i * step + c];
+    float t[kSumChains] = {};
+    const float* p = from + threadIdx.y * step + c;
+    step *= kSumRows;
+    int left = (static_cast<int>(n) - static_cast<int>(threadIdx.y) + kSumRows - 1) / kSumRows;
+    for (; left >= kSumChains; left -= kSumChains)
+#pragma unroll
+      for (int k = 0; k < kSumChains; ++k, p += step) t[k] += *p;
+    if (left >= kSumChains / 2) {
+#pragma unroll
+      for (int k = 0; k < kSumChains / 2; ++k, p += step) t[k] += *p;
+      left -= kSumChains / 2;
+    }
+#pragma unroll 1
+    for (; left > 0; --left, p += step) t[kSumChains - 1] += *p;
+#pragma unroll
+    for (int w = kSumChains / 2; w > 0; w /= 2)
+#pragma unroll
+      for (int k = 0; k < w; ++k) t[k] += t[k + w];
+    s = extra && threadIdx.y == 0 ? extra[c] + t[0] : t[0];
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -983,30 +1006,45 @@ Shape shape_for(int C, int max_nv) {
 struct Ring {
   int threads, stages, ctas, bytes;
 };
-Ring ring_for(int C, int stage, int ctas) {
+Ring ring_for(int C, int nv, int stage, int ctas) {
   Ring r;
-  r.threads = round_up((C + 8 * kRingNv - 1) / (8 * kRingNv), 32);
-  const int own = 2 * own_weight_bytes(r.threads);
+  r.threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
+  const int own = 2 * own_weight_bytes(r.threads, nv);
   r.ctas = std::max(1, std::min(ctas, kRingBytes / (own + 2 * stage)));
   r.stages = std::max(2, std::min(kMaxRing, (kRingBytes / r.ctas - own) / stage));
   r.bytes = own + r.stages * stage;
   return r;
 }
-Ring fwd_ring(int C, int elem) { return ring_for(C, 2 * ring_row(C, elem), C <= 4096 ? 3 * 256 / round_up((C + 15) / 16, 32) : 1); }
-Ring bwd_ring(int C, int elem) { return ring_for(C, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1); }
-
-// Whether the ring serves rows of this width with `arrays` arrays (two stages fit).
-bool ring_serves(int C, int elem, int arrays) {
-  return C > kRingLow && C <= kRingHigh && 2 * (own_weight_bytes(round_up((C + 15) / 16, 32)) + arrays * ring_row(C, elem)) <= kRingBytes;
+Ring fwd_ring(int C, int elem) {
+  const int nv = elem == 4 ? 1 : 2, most = nv == 1 ? 2 * 512 : 3 * 256;  // threads of an SM
+  return ring_for(C, nv, 2 * ring_row(C, elem), C <= 4096 ? most / round_up((C + 8 * nv - 1) / (8 * nv), 32) : 1);
+}
+Ring bwd_ring(int C, int elem) {
+  return ring_for(C, kBwdNv, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1);
 }
 
-// Below two rows an SM there is nothing to request ahead, and the plain kernels start sooner.
-bool many_rows(int64_t rows) { return rows > 2 * current_sm_count(); }
+// Whether a ring of rows of this width has room (two stages fit).
+bool ring_serves(int C, const Ring& r) { return C > kRingLow && C <= kRingHigh && r.bytes <= kRingBytes; }
+
+// Whether there is enough to request ahead: below that the plain kernels start sooner.  Measured with rows in L2, ring
+// against plain: forward bf16 2000 x 2000 8.4 us against 8.2, 1200 x 4000 9.1 against 10.9, fp32 600 x 4000 11.1 against 10.8,
+// 1200 x 4000 17 against 20; backward bf16 450 x 2000 15.1 against 13.9, 600 x 2000 14.3 against 15.6, bf16
+// 1200 x 2001 23.3 against 23.0, fp32 1200 x 2000 23.4 against 21.8, 2000 x 2000 28.9 against 31.8.
+bool fwd_ring_pays(int64_t rows, int C, int elem) {
+  const int64_t sms = current_sm_count();
+  return rows > 2 * sms && rows * C * elem >= 65536 * sms;
+}
+bool bwd_ring_pays(int64_t rows, int C, int elem, bool vec) {
+  const int64_t sms = current_sm_count();
+  return rows > 2 * sms && rows * C >= (vec && elem == 2 ? 8192 : 16384) * sms;
+}
 
 int64_t bwd_ctas(const bconv_block_norm_desc_t* d, int64_t* rows_per_cta) {
   const int elem = dtype_bytes(d->dtype);
-  const int64_t most =
-      static_cast<int64_t>(current_sm_count()) * (ring_serves(d->width, elem, 4) ? bwd_ring(d->width, elem).ctas : 2);
+  // (rows of one warp: 16 CTAs an SM, 16000 x 111 bf16 in 25 us, 167 with two)
+  const Ring r = bwd_ring(d->width, elem);
+  const int per_sm = ring_serves(d->width, r) ? r.ctas : d->width <= kRingLow ? 16 : 2;
+  const int64_t most = static_cast<int64_t>(current_sm_count()) * per_sm;
   const int64_t per = std::max<int64_t>(1, ceil_div(d->rows, most));
   if (rows_per_cta) *rows_per_cta = per;
   return d->rows > 0 ? ceil_div(d->rows, per) : 0;
@@ -1054,10 +1092,11 @@ cudaError_t launch_ring(Kern kern, const Args& a, int64_t ctas, const Ring& r, c
 
 template <typename T, bool VEC>
 cudaError_t launch_fwd_ring(const FwdArgs& a, cudaStream_t s) {
+  constexpr int kNv = sizeof(T) == 4 ? 1 : 2, kFew = 512 / kNv;
   const Ring r = fwd_ring(a.C, sizeof(T));
   const int64_t ctas = std::min(a.rows, static_cast<int64_t>(current_sm_count()) * r.ctas);
-  if (r.threads <= 256) return launch_ring(block_norm_fwd_ring_kernel<T, VEC, 256>, a, ctas, r, s);
-  return launch_ring(block_norm_fwd_ring_kernel<T, VEC, 512>, a, ctas, r, s);
+  if (r.threads <= kFew) return launch_ring(block_norm_fwd_ring_kernel<T, VEC, kNv, kFew>, a, ctas, r, s);
+  return launch_ring(block_norm_fwd_ring_kernel<T, VEC, kNv, 2 * kFew>, a, ctas, r, s);
 }
 
 template <typename T, bool VEC>
@@ -1122,7 +1161,8 @@ bconv_status_t bconv_block_norm_forward(const bconv_block_norm_desc_t* d, const 
             d->rows,  gate ? d->rows_per_gate : 1, d->width, d->residual_scale, d->eps};
   const bool vec = d->width % 8 == 0 &&
                    all_aligned16({residual, block, gate, post_weight, pre_weight, residual_out, normed});
-  if (many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 2))
+  const int elem = dtype_bytes(d->dtype);
+  if (fwd_ring_pays(d->rows, d->width, elem) && ring_serves(d->width, fwd_ring(d->width, elem)))
     return from_cuda(with_dtype(d->dtype, [&](auto t) {
       using T = decltype(t);
       return vec ? launch_fwd_ring<T, true>(a, stream) : launch_fwd_ring<T, false>(a, stream);
@@ -1178,10 +1218,8 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   const bool vec = d->width % 8 == 0 && all_aligned16({residual_out, block, gate, d_residual_out, d_normed, post_weight,
                                                        pre_weight, d_residual, d_block, d_gate, workspace});
   const Shape sh = shape_for(d->width, 4);
-  // Unaligned fp32 rows up to 4096 channels are left to the plain kernel, which keeps all its sums in registers (8000 x
-  // 2001: 173 us against 322; 16-bit rows 247 against 238, 8000 x 4099 fp32 1023 against 624).
-  const bool ring = many_rows(d->rows) && ring_serves(d->width, dtype_bytes(d->dtype), 4) &&
-                    (vec || d->dtype != BCONV_DTYPE_F32 || d->width > 4096);
+  const int elem = dtype_bytes(d->dtype);
+  const bool ring = bwd_ring_pays(d->rows, d->width, elem, vec) && ring_serves(d->width, bwd_ring(d->width, elem));
   e = with_dtype(d->dtype, [&](auto t) {
     using T = decltype(t);
     if (ring) return vec ? launch_bwd_ring<T, true>(a, ctas, stream) : launch_bwd_ring<T, false>(a, ctas, stream);
@@ -1195,8 +1233,8 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   const int64_t gates = d_gate ? ceil_div(a.rows, a.per_gate) : 0;
   f.by_gate = gates < ctas;
   const unsigned ys = static_cast<unsigned>(2 + (f.by_gate ? gates : ctas - 1));
-  block_norm_sum_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.C, 32)), ys), dim3(32, kSumRows), 0, stream>>>(f);
-  return from_cuda(cudaGetLastError());
+  return from_cuda(launch_overlapped(block_norm_sum_kernel, dim3(static_cast<unsigned>(ceil_div(a.C, 32)), ys), dim3(32, kSumRows),
+                                     0, stream, f));
 }
 
 }  // extern "C"

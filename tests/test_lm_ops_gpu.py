@@ -507,6 +507,60 @@ def test_block_norm_in_place_over_many_rows(width, dtype):
         assert all(torch.equal(x, y) for x, y in zip((*to, *sums), want))
 
 
+# enough rows for the kernels that request rows ahead: whole and odd widths, gates cut anywhere
+RING_SHAPES = [(1303, 4000, 500), (1300, 4001, 0), (1302, 4003, 7), (2500, 2001, 100), (2501, 2000, 1), (610, 8191, 610),
+               (620, 8192, 0), (19000, 257, 0), (13003, 400, 77)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,per", RING_SHAPES)
+def test_block_norm_many_rows(rows, width, per, dtype):
+    test_block_norm(rows, width, per, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,per", RING_SHAPES)
+def test_block_norm_backward_many_rows(rows, width, per, dtype):
+    test_block_norm_backward(rows, width, per, dtype)
+
+
+@pytest.mark.parametrize("width", [1024, 1027])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_block_norm_many_rows_parts(width, dtype):
+    """Without a block, without the next norm, over the inputs: the same rows as a call of fewer rows gives."""
+    from binarized_convolution_b200 import _native as nat
+
+    rows, few = 5000, 200
+    r, b, pre, pw, _ = norm_inputs(41, rows, width, 0, dtype)
+    r64, b64, pre64, pw64 = opt64(r, b, pre, pw)
+    same, normed = bc.block_norm(r, pre_weight=pre)
+    assert torch.equal(same, r)
+    want = norm_ref(r64, None, pre64, None, None, 0, 1.0, 1e-6)[1]
+    close(normed, want, 2 * ROW * want.abs())
+    out, none = bc.block_norm(r, b, post_weight=pw)
+    assert none is None
+    want = norm_ref(r64, b64, None, pw64, None, 0, 1.0, 1e-6)[0]
+    close(out, want, ROW * (r64.abs() + (want - r64).abs()))
+    out, normed = bc.block_norm(r, b, pre_weight=pre, post_weight=pw)
+    code = {torch.float32: nat.DTYPE_F32, torch.bfloat16: nat.DTYPE_BF16, torch.float16: nat.DTYPE_F16}[dtype]
+    desc = nat.bconv_block_norm_desc_t(rows, 0, width, code, 1.0, 1e-6)
+    s = torch.cuda.current_stream().cuda_stream
+    r1, b1 = r.clone(), b.clone()
+    bc.bconv_block_norm_forward(desc, r1.data_ptr(), b1.data_ptr(), 0, pw.data_ptr(), pre.data_ptr(), b1.data_ptr(),
+                                r1.data_ptr(), s)
+    assert torch.equal(b1, out) and torch.equal(r1, normed)
+    do, dn = rnd(42, rows, width, dtype=dtype), rnd(43, rows, width, dtype=dtype)
+    got = bc.block_norm_backward(out, b, pre_weight=pre, post_weight=pw, d_residual_out=do, d_normed=dn)
+    grads, mags = norm_grad_ref(*opt64(out[-few:], b[-few:], pre, pw, None), 0, 1.0, 1e-6, *opt64(do[-few:], dn[-few:]))
+    for name in ("d_residual", "d_block"):  # (row by row)
+        close(getattr(got, name)[-few:], grads[name], 4 * ROW * mags[name])
+    ws = torch.empty(bc.bconv_block_norm_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    d1, d2 = do.clone(), dn.clone()
+    bc.bconv_block_norm_backward(desc, out.data_ptr(), b.data_ptr(), 0, pw.data_ptr(), pre.data_ptr(), d1.data_ptr(),
+                                 d2.data_ptr(), d2.data_ptr(), d1.data_ptr(), 0, 0, 0, ws.data_ptr(), s)
+    assert torch.equal(d2, got.d_residual) and torch.equal(d1, got.d_block)
+
+
 def test_block_norm_backward_asked_for_parts():
     """Any of the results may be left out, and the workspace where no sum over rows is wanted."""
     from binarized_convolution_b200 import _native as nat
