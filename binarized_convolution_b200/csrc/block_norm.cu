@@ -1082,11 +1082,11 @@ cudaError_t launch_bwd(const BwdArgs& a, int64_t ctas, int threads, cudaStream_t
   return cudaGetLastError();
 }
 
-template <typename Kern, typename Args>
-cudaError_t launch_ring(Kern kern, const Args& a, int64_t ctas, const Ring& r, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, r.bytes);
+template <auto Kern, typename Args>
+cudaError_t launch_ring(const Args& a, int64_t ctas, const Ring& r, cudaStream_t s) {
+  const cudaError_t e = allow_smem<Kern>(kRingBytes);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(ctas), r.threads, r.bytes, s>>>(a, r.stages);
+  Kern<<<static_cast<unsigned>(ctas), r.threads, r.bytes, s>>>(a, r.stages);
   return cudaGetLastError();
 }
 
@@ -1095,15 +1095,15 @@ cudaError_t launch_fwd_ring(const FwdArgs& a, cudaStream_t s) {
   constexpr int kNv = sizeof(T) == 4 ? 1 : 2, kFew = 512 / kNv;
   const Ring r = fwd_ring(a.C, sizeof(T));
   const int64_t ctas = std::min(a.rows, static_cast<int64_t>(current_sm_count()) * r.ctas);
-  if (r.threads <= kFew) return launch_ring(block_norm_fwd_ring_kernel<T, VEC, kNv, kFew>, a, ctas, r, s);
-  return launch_ring(block_norm_fwd_ring_kernel<T, VEC, kNv, 2 * kFew>, a, ctas, r, s);
+  if (r.threads <= kFew) return launch_ring<block_norm_fwd_ring_kernel<T, VEC, kNv, kFew>>(a, ctas, r, s);
+  return launch_ring<block_norm_fwd_ring_kernel<T, VEC, kNv, 2 * kFew>>(a, ctas, r, s);
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_bwd_ring(const BwdArgs& a, int64_t ctas, cudaStream_t s) {
   const Ring r = bwd_ring(a.C, sizeof(T));
-  if (r.threads <= 256) return launch_ring(block_norm_bwd_ring_kernel<T, VEC, 256>, a, ctas, r, s);
-  return launch_ring(block_norm_bwd_ring_kernel<T, VEC, 512>, a, ctas, r, s);
+  if (r.threads <= 256) return launch_ring<block_norm_bwd_ring_kernel<T, VEC, 256>>(a, ctas, r, s);
+  return launch_ring<block_norm_bwd_ring_kernel<T, VEC, 512>>(a, ctas, r, s);
 }
 
 // Calls f.operator()<T, NV, VEC, MAX_THREADS> for a row shape; the bound on the threads keeps the
