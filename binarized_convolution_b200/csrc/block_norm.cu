@@ -10,11 +10,14 @@
 //     q = a g dR;         db = bs (q w_post - b bs^2 mean(q w_post b))     (no norm: db = q)
 //     d_w_pre = sum_rows d_n r' rs;  d_w_post = sum_rows q b bs;  d_g = sum_rows a dR p
 //
-// Bound by HBM: the forward reads two and writes two arrays of rows x C, the backward reads four
-// and writes two; everything between stays in registers.  One CTA holds a whole row (its threads
-// 8 channels at a time), so each of the row sums is one block reduction, and the CTA walks over
-// rows with the weights in registers: fp32 weights re-read per row would be as many L2 bytes as
-// a bf16 row itself.
+// The forward reads two and writes two arrays of rows x C, the backward reads four and writes two, all of
+// them once.  One CTA holds a whole row (its threads 8 channels at a time), so each of the row sums is one block
+// reduction.  Few, narrow or very wide rows take the plain kernels, which hold a row in registers; many rows of
+// 257 to 8192 channels come ahead of their use through a ring in shared memory (below).
+// With many rows HBM is kept 50 to 80 % busy: two reductions a row, each behind a barrier, and as many warps as
+// the registers for sums and rows allow (the backward issues in 58 % of its cycles).  Rows in a graph, us: forward
+// 8192 x 4096 bf16 54, 4096 x 4096 fp32 47 (5.7 TB/s); backward 4096 x 4096 bf16 59, fp32 88 (4.6 TB/s), 8000 x
+// 2001 bf16 90.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>

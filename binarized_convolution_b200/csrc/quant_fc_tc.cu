@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) {
-              bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group.at, kQuantRows * 4, &B->ready[s]);
+              bulk_load(ring_s + ss * kScaleBytes + u * kQuantRows * 4, a.q.scale + group.at, kQuantRows * 4,
+                        &B->ready[s]);
               next_group(group);
             }
             ++issued;
@@ -723,8 +724,8 @@ struct Plan {
   int64_t tiles;
 };
 
-// Tokens per CTA and CTAs per tile, for `rows` rows of `parts` parts (one_tile: all rows in one tile).  A CTA's time for 128 input channels is about max(4 tokens,
-// kFloor) cycles: the MMAs, or reading and decoding 8 KB of codes.  Token counts that fill whole waves of
+// Tokens per CTA and CTAs per tile, for `rows` rows of `parts` parts (one_tile: all rows in one tile).  A CTA's time
+// for 128 input channels is about max(4 tokens, kFloor) cycles: the MMAs, or reading and decoding 8 KB of codes.  Token counts that fill whole waves of
 // CTAs win over large tiles with a ragged last wave; leftover SMs share the input channels.
 Plan plan_for(const QuantFcArgs& q, int64_t rows, int parts, int most_halves, bool one_tile) {
   constexpr int kFloor = 600;
