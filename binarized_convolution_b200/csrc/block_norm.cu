@@ -92,6 +92,7 @@ __device__ __forceinline__ void store8(T* row, int j, int C, const float (&v)[8]
 template <int MAX_WARPS, int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
   static_assert(N == 1 || N == 3, "");
+  constexpr int kWarps = MAX_WARPS <= 8 ? 8 : MAX_WARPS <= 16 ? 16 : 32;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   auto add = [](float x, int o) { return x + __shfl_xor_sync(0xffffffffu, x, o); };
   float z;
@@ -119,10 +120,10 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {  // four warps' sums a lane
-    const float4 f = *reinterpret_cast<const float4*>(buf + i * 32 + (lane & (MAX_WARPS / 4 - 1)) * 4);
+    const float4 f = *reinterpret_cast<const float4*>(buf + i * 32 + (lane & (kWarps / 4 - 1)) * 4);
     v[i] = (f.x + f.y) + (f.z + f.w);
 #pragma unroll
-    for (int o = MAX_WARPS / 8; o > 0; o >>= 1) v[i] = add(v[i], o);
+    for (int o = kWarps / 8; o > 0; o >>= 1) v[i] = add(v[i], o);
   }
 }
 // (The entries of warps that are not there; written before the first barrier of block_sums.)
@@ -611,7 +612,9 @@ __device__ __forceinline__ void put_gate_post(OwnWeights W, float alpha, const T
 // NV: 8-channel vectors of a thread.  Two, or one for fp32, whose rows leave room for only half as many CTAs (4096 x 4096:
 // 46.4 us against 50.1, 8000 x 2001: 50.3 against 60.6; bf16 30.1 against 28.5).
 template <typename T, bool VEC, int NV, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 3 : NV == 1 && MAX_THREADS == 512 ? 2 : 1)
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256                                      ? 3
+                                               : MAX_THREADS == 384 || (NV == 1 && MAX_THREADS == 512) ? 2
+                                                                                                       : 1)
     block_norm_fwd_ring_kernel(const FwdArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float sums[2][32];
@@ -1019,8 +1022,9 @@ Ring ring_for(int C, int nv, int stage, int ctas) {
   return r;
 }
 Ring fwd_ring(int C, int elem) {
-  const int nv = elem == 4 ? 1 : 2, most = nv == 1 ? 2 * 512 : 3 * 256;  // threads of an SM
-  return ring_for(C, nv, 2 * ring_row(C, elem), C <= 4096 ? most / round_up((C + 8 * nv - 1) / (8 * nv), 32) : 1);
+  const int nv = elem == 4 ? 1 : 2, threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
+  const int ctas = nv == 1 ? 2 * 512 / threads : threads <= 256 ? 3 * 256 / threads : threads <= 384 ? 2 : 1;
+  return ring_for(C, nv, 2 * ring_row(C, elem), ctas);
 }
 Ring bwd_ring(int C, int elem) {
   return ring_for(C, kBwdNv, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1);
@@ -1099,6 +1103,8 @@ cudaError_t launch_fwd_ring(const FwdArgs& a, cudaStream_t s) {
   const Ring r = fwd_ring(a.C, sizeof(T));
   const int64_t ctas = std::min(a.rows, static_cast<int64_t>(current_sm_count()) * r.ctas);
   if (r.threads <= kFew) return launch_ring<block_norm_fwd_ring_kernel<T, VEC, kNv, kFew>>(a, ctas, r, s);
+  if constexpr (kNv == 2)  // (8000 x 4099 bf16: 72 us, 100 with one CTA an SM; 6000 x 6144: 50, 60)
+    if (r.threads <= 384) return launch_ring<block_norm_fwd_ring_kernel<T, VEC, kNv, 384>>(a, ctas, r, s);
   return launch_ring<block_norm_fwd_ring_kernel<T, VEC, kNv, 2 * kFew>>(a, ctas, r, s);
 }
 

@@ -509,7 +509,7 @@ def test_block_norm_in_place_over_many_rows(width, dtype):
 
 # enough rows for the kernels that request rows ahead: whole and odd widths, gates cut anywhere
 RING_SHAPES = [(1303, 4000, 500), (1300, 4001, 0), (1302, 4003, 7), (2500, 2001, 100), (2501, 2000, 1), (610, 8191, 610),
-               (620, 8192, 0), (19000, 257, 0), (13003, 400, 77)]
+               (620, 8192, 0), (19000, 257, 0), (13003, 400, 77), (1303, 4104, 9), (1010, 6001, 0), (1013, 6144, 400)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
