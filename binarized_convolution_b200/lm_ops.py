@@ -5,12 +5,14 @@
 types, shapes and devices, allocate outputs and workspaces with torch and call the C entry points on
 the current stream of the tensors' device.  Activations are float32, bfloat16 or float16; inputs
 whose last dimension (or, where rows have to be packed, whose rows) are not contiguous are
-copied.  Gradients are explicit calls; nothing here records for autograd.
+copied.  Scalars are numbers; a one-element tensor given for one is read at the call, which waits for it.
+Gradients are explicit calls; nothing here records for autograd.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple
 
 import torch
@@ -75,6 +77,15 @@ def _like(t, device, dtype, shape, name):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _number(v, name):
+    """v as it is now: a one-element tensor is read (which waits for it), not kept."""
+    if type(v) is float:
+        return v
+    if isinstance(v, (str, bytes)):
+        raise TypeError(f"{name}: expected a number, got {v!r}")
+    return float(v.item() if isinstance(v, torch.Tensor) else v)
 
 
 def _rows(x):
@@ -215,9 +226,13 @@ class BlockNormGrad(NamedTuple):
     d_gate: torch.Tensor | None
 
 
-@functools.lru_cache(maxsize=256)
 def _norm_desc(device, rows, per, width, dtype, residual_scale, eps):
     """The C descriptor (by reference, and kept alive by its first item) and the backward's workspace on this device."""
+    return _norm_desc_of(device, rows, per, width, dtype, _number(residual_scale, "residual_scale"), _number(eps, "eps"))
+
+
+@functools.lru_cache(maxsize=256)  # (of plain numbers, which do not change behind its back)
+def _norm_desc_of(device, rows, per, width, dtype, residual_scale, eps):
     desc = nat.bconv_block_norm_desc_t(rows, per, width, _DTYPES[dtype], residual_scale, eps)
     with torch.cuda.device(device):
         need = nat.load_library().bconv_block_norm_workspace_bytes(desc)
@@ -317,9 +332,13 @@ class TokenLogprobs(NamedTuple):
     top_index: torch.Tensor | None
 
 
-@functools.lru_cache(maxsize=256)
 def _token_desc(rows, stride, vocab, dtype, top, temperature):
     """The C descriptor by reference (kept alive by the first item)."""
+    return _token_desc_of(rows, stride, vocab, dtype, operator.index(top), _number(temperature, "temperature"))
+
+
+@functools.lru_cache(maxsize=256)  # (of plain numbers, as above)
+def _token_desc_of(rows, stride, vocab, dtype, top, temperature):
     desc = nat.bconv_token_desc_t(rows, stride, vocab, _DTYPES[dtype], top, temperature)
     return desc, ctypes.byref(desc)
 
