@@ -539,13 +539,13 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const B
     ge = a.d_entropy[r];
     h = a.entropy[r];
   }
-  // d = p (k0 + k1 log p), and g / temperature more at the token
-  float k0 = -(g + ge * h) * scale, k1 = -ge * scale;
-  if (lse == -INFINITY) {  // nothing but -inf in the row: no gradient (a NaN of g stays)
+  if (lse == -INFINITY) {  // nothing but -inf in the row: no gradient, at the token either (a NaN of g stays)
     lse = 0.f;
-    k0 *= 0.f;
-    k1 = 0.f;
+    g *= 0.f;
+    ge *= 0.f;
   }
+  // d = p (k0 + k1 log p), and g / temperature more at the token
+  const float k0 = -(g + ge * h) * scale, k1 = -ge * scale;
   auto grad = [&](float v) {
     // (-inf: p = exp(kFar) = 0, with a finite product)
     const float logp = max_nan(fmaf(v, scale, -lse), kFar);

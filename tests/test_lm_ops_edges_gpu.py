@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import binarized_convolution_b200 as bc
-from test_lm_ops_gpu import norm_inputs, rnd
+from test_lm_ops_gpu import TYPES, norm_inputs, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,23 @@ def test_scalars_that_change_between_calls():
         with torch.no_grad():
             scalar.fill_(value)
         assert all(torch.equal(p, q) for p, q in zip(results(scalar), results(value)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_gradient_reaches_a_row_of_minus_infinity_alone(dtype):
+    """Its own token's entry included, wherever that lies: in whole 8-element steps or in front of and behind them."""
+    vocab = 1501
+    base = torch.full((3, vocab + 8), float("-inf"), dtype=dtype, device="cuda")
+    base[2] = 0.0
+    for first in (0, 3):
+        logits = base[:, first:first + vocab]
+        for token in (0, 1, 4, 700, vocab - 1):
+            tokens = torch.tensor([token, -1, token], device="cuda")
+            f = bc.token_logprobs(logits, tokens, temperature=0.5)
+            assert (f.lse[:2] == float("-inf")).all()
+            one = torch.ones(3, device="cuda")
+            for kw in (dict(d_logprob=one), dict(d_entropy=one), dict(d_logprob=one, d_entropy=one)):
+                d = bc.token_logprobs_backward(logits, tokens, f.lse, f.entropy, temperature=0.5, **kw)
+                assert (d[:2] == 0).all()
+                if "d_logprob" in kw:
+                    assert d[2, token] > 0
