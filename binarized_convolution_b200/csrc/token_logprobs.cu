@@ -27,6 +27,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.cuh"
@@ -578,6 +579,14 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const B
   }
 }
 
+// Whether operands of 4- and 8-byte elements (NULL allowed) are aligned to them.
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+  return true;
+}
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
 bconv_status_t check_desc(const bconv_token_desc_t* d) {
   if (!d || d->rows < 0 || d->rows > (int64_t{1} << 28) || d->vocab < 1 || d->vocab > (1 << 30) || d->stride < d->vocab ||
       !valid_dtype(d->dtype) || !(d->temperature > 0.f) || d->temperature > FLT_MAX || 1.f / d->temperature > FLT_MAX)
@@ -626,7 +635,8 @@ bconv_status_t bconv_token_logprobs_forward(const bconv_token_desc_t* d, const v
                                             int32_t* top_index, struct CUstream_st* stream) {
   const bconv_status_t st = check_desc(d);
   if (st != BCONV_OK) return st;
-  if (d->top < 0 || d->top > kMaxTop || d->top > d->vocab || (logprob && !tokens) || !aligned_elem(logits, d->dtype))
+  if (d->top < 0 || d->top > kMaxTop || d->top > d->vocab || (logprob && !tokens) || !aligned_elem(logits, d->dtype) ||
+      !aligned8(tokens) || !aligned4({logprob, entropy, lse, top_logprob, top_index}))
     return BCONV_ERR_INVALID_ARG;
   if (d->rows == 0) return BCONV_OK;
   if (!logits || (d->top > 0) != (top_logprob != nullptr) || (d->top > 0) != (top_index != nullptr))
@@ -643,7 +653,7 @@ bconv_status_t bconv_token_logprobs_backward(const bconv_token_desc_t* d, const 
   const bconv_status_t st = check_desc(d);
   if (st != BCONV_OK) return st;
   if (d_stride < d->vocab || (d_logprob && !tokens) || (d_entropy && !entropy) || !aligned_elem(logits, d->dtype) ||
-      !aligned_elem(d_logits, d->dtype) || (logits && logits == d_logits && d_stride != d->stride))
+      !aligned_elem(d_logits, d->dtype) || !aligned8(tokens) || !aligned4({lse, entropy, d_logprob, d_entropy}) || (logits && logits == d_logits && d_stride != d->stride))
     return BCONV_ERR_INVALID_ARG;
   if (d->rows == 0) return BCONV_OK;
   if (!logits || !lse || !d_logits) return BCONV_ERR_INVALID_ARG;

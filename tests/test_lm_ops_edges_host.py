@@ -3,6 +3,8 @@ change between calls, and refusals.  (Addresses below are never read.)"""
 import pytest
 import torch
 
+import binarized_convolution_b200 as bc
+from binarized_convolution_b200 import _native as nat
 from binarized_convolution_b200 import lm_ops
 
 
@@ -24,3 +26,19 @@ def test_a_scalar_given_as_a_tensor_is_read_at_every_call():
     for bad in (dict(temperature="1.0"), dict(temperature=None), dict(top=1.5)):
         with pytest.raises(TypeError):
             token(**bad)
+
+
+P, INVALID = 1 << 20, 1
+
+
+def test_token_logprobs_refuses_operands_off_their_elements_boundary():
+    lib = bc.load_library()
+    desc = nat.bconv_token_desc_t(4, 100, 100, nat.DTYPE_BF16, 5, 1.0)
+    calls = ((lib.bconv_token_logprobs_forward, 7, (), {1: 8}),        # logits, tokens, then floats and indexes
+             (lib.bconv_token_logprobs_backward, 7, (100,), {1: 8, 6: 2}))  # d_logits last, of the logits' type
+    for fn, count, rest, sizes in calls:
+        for at in range(count):
+            size = 2 if at == 0 else sizes.get(at, 4)
+            ptrs = [P] * count
+            ptrs[at] = P + size // 2
+            assert fn(desc, *ptrs, *rest, None) == INVALID, (fn.__name__, at)
