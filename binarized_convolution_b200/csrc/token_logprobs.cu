@@ -589,7 +589,7 @@ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0
 
 bconv_status_t check_desc(const bconv_token_desc_t* d) {
   if (!d || d->rows < 0 || d->rows > (int64_t{1} << 28) || d->vocab < 1 || d->vocab > (1 << 30) || d->stride < d->vocab ||
-      !valid_dtype(d->dtype) || !(d->temperature > 0.f) || d->temperature > FLT_MAX || 1.f / d->temperature > FLT_MAX)
+      !valid_dtype(d->dtype) || !(d->temperature > 0.f) || d->temperature > FLT_MAX || kLog2e / d->temperature > FLT_MAX)
     return BCONV_ERR_INVALID_ARG;
   return BCONV_OK;
 }

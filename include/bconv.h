@@ -483,7 +483,7 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* desc, co
 typedef struct {
   int64_t rows, stride;
   int32_t vocab, dtype, top;
-  float temperature; /* finite, > 0 */
+  float temperature; /* finite, > 0, and log2(e) / temperature finite too */
 } bconv_token_desc_t;
 
 bconv_status_t bconv_token_logprobs_forward(const bconv_token_desc_t* desc, const void* logits, const int64_t* tokens,

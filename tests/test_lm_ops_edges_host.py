@@ -42,3 +42,14 @@ def test_token_logprobs_refuses_operands_off_their_elements_boundary():
             ptrs = [P] * count
             ptrs[at] = P + size // 2
             assert fn(desc, *ptrs, *rest, None) == INVALID, (fn.__name__, at)
+
+
+def test_token_logprobs_refuses_temperatures_whose_inverse_overflows():
+    """Also where 1 / temperature is finite but log2(e) / temperature is not: from 2.94e-39 to 4.24e-39."""
+    lib = bc.load_library()
+    for temperature in (1e-45, 2.9e-39, 3e-39, 4.2e-39):
+        desc = nat.bconv_token_desc_t(4, 100, 100, nat.DTYPE_BF16, 5, temperature)
+        assert lib.bconv_token_logprobs_forward(desc, *[P] * 7, None) == INVALID, temperature
+        assert lib.bconv_token_logprobs_backward(desc, *[P] * 7, 100, None) == INVALID, temperature
+    desc = nat.bconv_token_desc_t(0, 100, 100, nat.DTYPE_BF16, 5, 4.3e-39)
+    assert lib.bconv_token_logprobs_forward(desc, *[P] * 7, None) == 0
