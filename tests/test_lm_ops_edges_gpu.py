@@ -46,3 +46,27 @@ def test_no_gradient_reaches_a_row_of_minus_infinity_alone(dtype):
                 assert (d[:2] == 0).all()
                 if "d_logprob" in kw:
                     assert d[2, token] > 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(3001, 1003), (1302, 4003)])
+def test_block_norm_first_and_last_row_of_unaligned_arrays_stay_in_their_rows(rows, width, dtype):
+    """Rows off 16-byte boundaries are copied in 16-byte pieces, but for the edges of the first and the last row;
+    later rows in the same place of shared memory must not see those edges."""
+    r, b, pre, post, _ = norm_inputs(rows, rows, width, 0, dtype)
+    do, dn = rnd(1, rows, width, dtype=dtype), rnd(2, rows, width, dtype=dtype)
+    kw = dict(pre_weight=pre, post_weight=post)
+    arrays = [torch.empty(rows * width + 1, dtype=dtype, device="cuda")[1:].view(rows, width) for _ in range(4)]
+    results = []
+    for edge in (1.0, 1000.0):
+        for array, values in zip(arrays, (r, b, do, dn)):
+            array.copy_(values)
+            array[0].mul_(edge)
+            array[-1].mul_(edge)
+        r1, b1, do1, dn1 = arrays
+        first = bc.block_norm(r1, b1, **kw)[:2] + bc.block_norm_backward(r1, b1, d_residual_out=do1, d_normed=dn1, **kw)[:2]
+        for _ in range(5):
+            again = bc.block_norm(r1, b1, **kw)[:2] + bc.block_norm_backward(r1, b1, d_residual_out=do1, d_normed=dn1, **kw)[:2]
+            assert all(torch.equal(p, q) for p, q in zip(first, again))
+        results.append(first)
+    assert all(torch.equal(p[1:-1], q[1:-1]) for p, q in zip(*results))
