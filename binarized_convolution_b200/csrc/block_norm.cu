@@ -483,6 +483,9 @@ __device__ __forceinline__ void ring_request(uint64_t* full, uint8_t* to, const 
     for (int i = 0; i < N; ++i)
       if (src[i]) tcdev::bulk_load(to + i * pitch, src[i] + row * C, bytes, full);
   } else {
+    // The plain stores of an earlier request come before these copies, which may write the same places.  (A fence in the
+    // branches of those stores instead: 8000 x 2001 bf16 backward 69 us, not 61.)
+    tcdev::fence_proxy_async();
     uint32_t sum = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -497,8 +500,6 @@ __device__ __forceinline__ void ring_request(uint64_t* full, uint8_t* to, const 
           for (int c = 0; reinterpret_cast<uintptr_t>(p + c) < lo; ++c) at[c] = p[c];
         if (hi < e)
           for (int c = static_cast<int>(reinterpret_cast<const T*>(hi) - p); c < C; ++c) at[c] = p[c];
-        // (a later row's bulk copy may write where these plain stores did)
-        if (lo > a || hi < e) tcdev::fence_proxy_async();
         tcdev::bulk_load(to + i * pitch + (lo - base), reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), full);
         sum += static_cast<uint32_t>(hi - lo);
       }
