@@ -44,6 +44,7 @@ from ._native import (  # noqa: F401
     bconv_block_norm_backward,
     bconv_block_norm_desc_t,
     bconv_block_norm_forward,
+    bconv_block_norm_sync_status,
     bconv_block_norm_workspace_bytes,
     bconv_create,
     bconv_cta_mode,

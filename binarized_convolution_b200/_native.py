@@ -130,6 +130,7 @@ _SIGS = {
     "bconv_block_norm_forward": (_I32, [ctypes.POINTER(bconv_block_norm_desc_t)] + [_P] * 8),
     "bconv_block_norm_workspace_bytes": (_I64, [ctypes.POINTER(bconv_block_norm_desc_t)]),
     "bconv_block_norm_backward": (_I32, [ctypes.POINTER(bconv_block_norm_desc_t)] + [_P] * 14),
+    "bconv_block_norm_sync_status": (_I32, [_P]),
     "bconv_token_logprobs_forward": (_I32, [ctypes.POINTER(bconv_token_desc_t)] + [_P] * 8),
     "bconv_token_logprobs_backward": (_I32, [ctypes.POINTER(bconv_token_desc_t)] + [_P] * 7 + [_I64, _P]),
 }
@@ -493,6 +494,11 @@ def bconv_block_norm_backward(desc: bconv_block_norm_desc_t, residual_out_ptr, b
                                                   workspace_ptr, stream)
     if st:
         raise BconvError(st, "bconv_block_norm_backward")
+
+
+def bconv_block_norm_sync_status(stream: int = 0):
+    """Waits for the stream; raises if a block norm on the current device gave up a wait since the last report."""
+    _check(load_library().bconv_block_norm_sync_status(stream), "bconv_block_norm_sync_status")
 
 
 def bconv_token_logprobs_forward(desc: bconv_token_desc_t, logits_ptr, tokens_ptr, logprob_ptr, entropy_ptr, lse_ptr,

@@ -448,18 +448,29 @@ constexpr int kRingBytes = 216 * 1024;           // of an SM
 constexpr int kMaxRing = 4;
 constexpr int kBwdNv = 2;                        // 8-channel vectors of a thread (one: 81 us for 4096 x 4096, not 58)
 
-// (Copies that were issued always arrive; the limit of a second only keeps a wait from being endless.)
-__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity) {
-  if (tcdev::mbar_try(bar, parity)) return;
-  uint64_t t0 = 0;
-  while (true) {
+// Set when a ring gave up a wait: reported, and cleared, by bconv_block_norm_sync_status.
+__device__ uint32_t block_norm_error;
+
+__device__ __forceinline__ bool ring_gave_up(const uint32_t* gave_up) {
+  return *reinterpret_cast<const volatile uint32_t*>(gave_up) != 0;
+}
+// Copies that were issued arrive, so a wait ends.  After a second it gives up all the same: it sets the error word and
+// the CTA's flag, with which no further row is requested or waited for.  (The other copies in flight are as old by
+// then.)  Out of line, it costs the backward no registers (4096 x 4096 bf16 58.1 us, 59.3 with it inline).
+__device__ __noinline__ void ring_wait_slow(uint64_t* bar, uint32_t parity, uint32_t* gave_up) {
+  const uint64_t t0 = tcdev::globaltimer();
+  while (!ring_gave_up(gave_up)) {
 #pragma unroll 1
     for (int i = 0; i < 1024; ++i)
       if (tcdev::mbar_try(bar, parity)) return;
-    const uint64_t t = tcdev::globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > tcdev::kTimeoutNs) return;
+    if (tcdev::globaltimer() - t0 > tcdev::kTimeoutNs) {
+      atomicOr(&block_norm_error, kErrTimeout);
+      atomicExch(gave_up, 1u);
+    }
   }
+}
+__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity, uint32_t* gave_up) {
+  if (!tcdev::mbar_try(bar, parity)) ring_wait_slow(bar, parity, gave_up);
 }
 
 // Bytes of a row in a stage: the 16-byte pieces that may hold it.
@@ -514,8 +525,9 @@ __device__ __forceinline__ const T* ring_at(const uint8_t* stage, int i, const T
   return reinterpret_cast<const T*>(stage + i * ring_row(C, sizeof(T)) + shift);
 }
 
-__device__ __forceinline__ void ring_init(uint64_t* full, int stages) {
+__device__ __forceinline__ void ring_init(uint64_t* full, int stages, uint32_t* gave_up) {
   if (threadIdx.x == 0) {
+    *gave_up = 0;
     for (int s = 0; s < stages; ++s) tcdev::mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -622,13 +634,14 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256               
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float sums[2][32];
   __shared__ uint64_t full[kMaxRing];
+  __shared__ uint32_t gave_up;
   clear_sums(sums);
   const bool all = whole<NV>(a.C);
   const int C = a.C, stage_bytes = 2 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x, NV);
   OwnWeights pre{reinterpret_cast<float4*>(smem)}, gate_post{reinterpret_cast<float4*>(smem + own)};
   uint8_t* const ring = smem + 2 * own;
   const float inv = 1.f / static_cast<float>(C);
-  ring_init(full, stages);
+  ring_init(full, stages, &gave_up);
   const int64_t step = gridDim.x;
   const T* const src[2] = {static_cast<const T*>(a.residual), static_cast<const T*>(a.block)};
   if (threadIdx.x < 32 && tcdev::elect_one())
@@ -649,7 +662,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256               
   for (int64_t row = blockIdx.x; row < a.rows; row += step) {
     if (a.gate && row >= gate_row.end)
       put_gate_post<T, VEC, NV>(gate_post, a.alpha, static_cast<const T*>(a.gate) + gate_row.of(row, a.per_gate) * C, a.post, C);
-    ring_wait(&full[s], parity);
+    ring_wait(&full[s], parity, &gave_up);
     uint8_t* const stage = ring + s * stage_bytes;
     const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const b_row = ring_at<T, VEC>(stage, 1, src[1], C, row);
     uint64_t r[NV][4], b[NV][4], qq = 0;
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256               
     float q[1] = {both(qq)};
     if (a.post) block_sums<MAX_THREADS / 32>(q, sums[0]);
     else __syncthreads();
-    if (threadIdx.x < 32 && row + stages * step < a.rows && tcdev::elect_one())  // everyone has read this stage
+    if (threadIdx.x < 32 && row + stages * step < a.rows && tcdev::elect_one() && !ring_gave_up(&gave_up))  // everyone has read this stage
       ring_request<T, VEC>(&full[s], stage, src, C, row + stages * step, a.rows);
     __syncwarp();
     if (++s == stages) {
@@ -733,6 +746,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float sums[2][3 * 32];
   __shared__ uint64_t full[kMaxRing];
+  __shared__ uint32_t gave_up;
   clear_sums(sums);
   const bool all = whole<NV>(a.C);
   const int C = a.C, stage_bytes = 4 * ring_row(C, sizeof(T)), own = own_weight_bytes(blockDim.x, NV);
@@ -740,7 +754,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
   uint8_t* const ring = smem + 2 * own;
   const float inv = 1.f / static_cast<float>(C);
   const int64_t first = blockIdx.x * a.rows_per_cta, last = min(first + a.rows_per_cta, a.rows), cta = blockIdx.x;
-  ring_init(full, stages);
+  ring_init(full, stages, &gave_up);
   const T* const src[4] = {a.d_normed ? static_cast<const T*>(a.residual_out) : nullptr,
                            static_cast<const T*>(a.d_normed), static_cast<const T*>(a.d_out),
                            static_cast<const T*>(a.block)};
@@ -808,7 +822,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
         else gate_to = a.d_gate + g * C;
       }
     }
-    ring_wait(&full[s], parity);
+    ring_wait(&full[s], parity, &gave_up);
     uint8_t* const stage = ring + s * stage_bytes;
     const T *const r_row = ring_at<T, VEC>(stage, 0, src[0], C, row), *const dn_row = ring_at<T, VEC>(stage, 1, src[1], C, row),
             *const do_row = ring_at<T, VEC>(stage, 2, src[2], C, row), *const b_row = ring_at<T, VEC>(stage, 3, src[3], C, row);
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 2 : 1) block
     float t[3] = {both(tr), both(tu), both(tb)};
     block_sums<MAX_THREADS / 32>(t, sums[0]);
     const int64_t next = row - 1 + stages;
-    if (threadIdx.x < 32 && row > first && next < last && tcdev::elect_one()) {
+    if (threadIdx.x < 32 && row > first && next < last && tcdev::elect_one() && !ring_gave_up(&gave_up)) {
       const int sp = s == 0 ? stages - 1 : s - 1;
       ring_request<T, VEC>(&full[sp], ring + sp * stage_bytes, src, C, next, a.rows);
     }
@@ -1247,6 +1261,20 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   const unsigned ys = static_cast<unsigned>(2 + (f.by_gate ? gates : ctas - 1));
   return from_cuda(launch_overlapped(block_norm_sum_kernel, dim3(static_cast<unsigned>(ceil_div(a.C, 32)), ys), dim3(32, kSumRows),
                                      0, stream, f));
+}
+
+bconv_status_t bconv_block_norm_sync_status(struct CUstream_st* stream) {
+  uint32_t err = 0;
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&err, block_norm_error, sizeof(err));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return from_cuda(e);
+  }
+  if (!err) return BCONV_OK;
+  const uint32_t none = 0;
+  e = cudaMemcpyToSymbol(block_norm_error, &none, sizeof(none));
+  return e != cudaSuccess ? from_cuda(e) : err & kErrTimeout ? BCONV_ERR_TIMEOUT : BCONV_ERR_CUDA;
 }
 
 }  // extern "C"

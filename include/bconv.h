@@ -464,6 +464,9 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* desc, co
                                          const float* pre_weight, const void* d_residual_out, const void* d_normed,
                                          void* d_residual, void* d_block, float* d_pre_weight, float* d_post_weight,
                                          float* d_gate, void* workspace, struct CUstream_st* stream);
+/* Waits for `stream` and reports whether a block norm of the current device gave up a wait since the last
+ * report (TIMEOUT: rows of its results are missing), as the layers' *_sync_status do. */
+bconv_status_t bconv_block_norm_sync_status(struct CUstream_st* stream);
 
 /*
  * What rows of logits say.  With x = logits / temperature, per row:

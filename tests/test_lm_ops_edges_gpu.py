@@ -70,3 +70,21 @@ def test_block_norm_first_and_last_row_of_unaligned_arrays_stay_in_their_rows(ro
             assert all(torch.equal(p, q) for p, q in zip(first, again))
         results.append(first)
     assert all(torch.equal(p[1:-1], q[1:-1]) for p, q in zip(*results))
+
+
+@pytest.mark.parametrize("width", [1024, 1027])
+def test_block_norm_status_of_the_waits(width):
+    """Whether a kernel that requests rows ahead gave up a wait comes back from the status call, and a graph's
+    replays report to the same place."""
+    rows = 3000
+    r, b, pre, post, _ = norm_inputs(3, rows, width, 0, torch.bfloat16)
+    stream = torch.cuda.current_stream().cuda_stream
+    out = bc.block_norm(r, b, pre_weight=pre, post_weight=post)
+    bc.bconv_block_norm_sync_status(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = bc.block_norm(r, b, pre_weight=pre, post_weight=post)
+        bc.block_norm_backward(r, b, pre_weight=pre, post_weight=post, d_normed=r)
+    graph.replay()
+    bc.bconv_block_norm_sync_status(stream)
+    assert all(torch.equal(p, q) for p, q in zip(out, held))

@@ -53,3 +53,10 @@ def test_token_logprobs_refuses_temperatures_whose_inverse_overflows():
         assert lib.bconv_token_logprobs_backward(desc, *[P] * 7, 100, None) == INVALID, temperature
     desc = nat.bconv_token_desc_t(0, 100, 100, nat.DTYPE_BF16, 5, 4.3e-39)
     assert lib.bconv_token_logprobs_forward(desc, *[P] * 7, None) == 0
+
+
+def test_block_norm_status_needs_a_device():
+    if torch.cuda.is_available():
+        pytest.skip("a CUDA device is present")
+    with pytest.raises(bc.BconvError):
+        bc.bconv_block_norm_sync_status()
