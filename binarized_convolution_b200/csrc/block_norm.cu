@@ -1081,6 +1081,11 @@ bconv_status_t check_desc(const bconv_block_norm_desc_t* d) {
   return d->width > kMaxWidth ? BCONV_ERR_UNSUPPORTED : BCONV_OK;
 }
 
+// Rows that share a gate row: no more than there are (sums with larger numbers could overflow).
+int64_t per_gate(const bconv_block_norm_desc_t* d, const void* gate) {
+  return gate ? std::min(d->rows_per_gate, d->rows) : 1;
+}
+
 bool all_aligned16(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (!aligned16(p)) return false;
@@ -1184,7 +1189,7 @@ bconv_status_t bconv_block_norm_forward(const bconv_block_norm_desc_t* d, const 
     return BCONV_ERR_INVALID_ARG;
   if (!residual) return BCONV_ERR_INVALID_ARG;
   FwdArgs a{residual, block, gate, post_weight, pre_weight, residual_out, normed,
-            d->rows,  gate ? d->rows_per_gate : 1, d->width, d->residual_scale, d->eps};
+            d->rows,  per_gate(d, gate), d->width, d->residual_scale, d->eps};
   const bool vec = d->width % 8 == 0 &&
                    all_aligned16({residual, block, gate, post_weight, pre_weight, residual_out, normed});
   const int elem = dtype_bytes(d->dtype);
@@ -1239,7 +1244,7 @@ bconv_status_t bconv_block_norm_backward(const bconv_block_norm_desc_t* d, const
   a.sum_post = d_post_weight ? ws + part : nullptr;
   a.sum_gate = d_gate ? ws + 2 * part : nullptr;
   a.d_gate = d_gate;
-  a.rows = d->rows; a.per_gate = gate ? d->rows_per_gate : 1; a.rows_per_cta = rows_per_cta;
+  a.rows = d->rows; a.per_gate = per_gate(d, gate); a.rows_per_cta = rows_per_cta;
   a.C = d->width; a.alpha = d->residual_scale; a.eps = d->eps;
   const bool vec = d->width % 8 == 0 && all_aligned16({residual_out, block, gate, d_residual_out, d_normed, post_weight,
                                                        pre_weight, d_residual, d_block, d_gate, workspace});

@@ -88,3 +88,21 @@ def test_block_norm_status_of_the_waits(width):
     graph.replay()
     bc.bconv_block_norm_sync_status(stream)
     assert all(torch.equal(p, q) for p, q in zip(out, held))
+
+
+def test_block_norm_gate_of_more_rows_than_there_are():
+    """rows_per_gate up to the largest int64: one gate row for all rows."""
+    rows, width = 2500, 96
+    out, b, pre, post, _ = norm_inputs(5, rows, width, 0, torch.float32)
+    g, d = rnd(6, 1, width), rnd(7, rows, width)
+
+    def run(per):
+        kw = dict(pre_weight=pre, post_weight=post, gate=g, rows_per_gate=per)
+        return (*bc.block_norm(out, b, **kw), *bc.block_norm_backward(out, b, d_normed=d, **kw))
+
+    want = run(rows)
+    for per in (rows + 1, 1 << 62, (1 << 63) - rows, (1 << 63) - 1):
+        # (what the allocator may hand out again)
+        poison = [torch.full((1, width), float("nan"), device="cuda") for _ in range(64)]
+        del poison
+        assert all(torch.equal(p, q) for p, q in zip(run(per), want)), per
