@@ -261,10 +261,12 @@ def _block_norm_args(residual, block, pre_weight, post_weight, gate, rows_per_ga
         if not isinstance(gate, torch.Tensor) or gate.dim() < 1 or gate.shape[-1] != width:
             raise ValueError(f"gate: expected [..., {width}]")
         gates = gate.numel() // width
-        per = rows // gates if rows_per_gate is None and gates else (rows_per_gate or 1)
-        if per < 1 and rows:
+        if rows_per_gate is not None:
+            per = operator.index(rows_per_gate)
+        elif rows:
+            per = rows // max(gates, 1)
+        if per < 1:
             raise ValueError("rows_per_gate must be positive, and there are not more gates than rows")
-        per = max(per, 1)
         if gates != -(-rows // per):
             raise ValueError(f"{gates} gate rows of {per} rows each do not fit {rows} rows")
         gate = _like(gate, device, dtype, gate.shape, "gate")

@@ -106,3 +106,17 @@ def test_block_norm_gate_of_more_rows_than_there_are():
         poison = [torch.full((1, width), float("nan"), device="cuda") for _ in range(64)]
         del poison
         assert all(torch.equal(p, q) for p, q in zip(run(per), want)), per
+
+
+def test_block_norm_rows_per_gate_is_a_positive_number_read_at_every_call():
+    r, b, _, _, g = norm_inputs(8, 6, 32, 1, torch.float32)
+    for bad in (0, -2):
+        with pytest.raises(ValueError):
+            bc.block_norm(r, b, gate=g, rows_per_gate=bad)
+    with pytest.raises(TypeError):
+        bc.block_norm(r, b, gate=g, rows_per_gate=1.0)
+    per = torch.tensor(1)
+    for n in (1, 2, 3):
+        per.fill_(n)
+        got = bc.block_norm(r, b, gate=g[:6 // n], rows_per_gate=per).residual_out
+        assert torch.equal(got, bc.block_norm(r, b, gate=g[:6 // n].repeat_interleave(n, 0)).residual_out)
