@@ -27,7 +27,9 @@ def _require_cuda(x):
     return x.contiguous()
 
 
-class _Layer:
+class _Owner:
+    """Owns a handle of the library."""
+
     _destroy = None
 
     def close(self):
@@ -41,6 +43,14 @@ class _Layer:
         except Exception:  # noqa: BLE001 -- interpreter shutdown
             pass
 
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class _Layer(_Owner):
     # ---- chained binary layers (bit-packed activations; see bconv_forward_io) ----
     def set_output_terms(self, next_in_scale=None, next_in_bias=None):
         """The input terms of the layer that will read this layer's bit-packed output."""
@@ -80,12 +90,6 @@ class _Layer:
         out = torch.empty(self.out_dims, dtype=torch.float32, device=x_bits.device)
         self.forward_io(x_bits=x_bits, x_a=x_a, out=out)
         return out
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        self.close()
 
 
 class BinaryConv2d(_Layer):

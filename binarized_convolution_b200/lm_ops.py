@@ -18,7 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import _native as nat
-from .layers import _Layer
+from .layers import _Owner
 
 _DTYPES = {torch.float32: nat.DTYPE_F32, torch.bfloat16: nat.DTYPE_BF16, torch.float16: nat.DTYPE_F16}
 _NAMED = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -99,7 +99,7 @@ def _rows(x):
     return x, x.numel() // width if width else 0, width
 
 
-class QuantFC(_Layer):
+class QuantFC(_Owner):
     """A fully-connected layer with 4-bit weights and group scales on the current CUDA device.
 
     ``W[c][f] = scale[c][f // group_size] * (code[c][f] - zero[c][f // group_size])``.

@@ -60,3 +60,11 @@ def test_block_norm_status_needs_a_device():
         pytest.skip("a CUDA device is present")
     with pytest.raises(bc.BconvError):
         bc.bconv_block_norm_sync_status()
+
+
+def test_a_quant_fc_has_no_methods_of_the_bit_packed_layers():
+    for name in ("forward_io", "set_output_terms", "bits_shape", "forward_to_bits", "forward_from_bits"):
+        assert not hasattr(bc.QuantFC, name), name
+        assert hasattr(bc.BinaryConv2d, name) and hasattr(bc.BinaryFC, name), name
+    for name in ("close", "__enter__", "__exit__", "sync_status", "forward_into"):
+        assert hasattr(bc.QuantFC, name), name
