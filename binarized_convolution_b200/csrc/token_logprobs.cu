@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) token_logprobs_fwd_kernel(con
   __syncthreads();
   st = S.stat[0];
   const bool nothing = st.m == -INFINITY && st.s == 0.f;
-  const float log2_s = __log2f(st.s);
+  const float log2_s = log2f(st.s);  // (the hardware's is off by 2^-22 near 1: nearly certain tokens)
   auto logprob = [&](float v) {
     if (st.s != st.s) return st.s;
     if (nothing || v == -INFINITY) return -INFINITY;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import binarized_convolution_b200 as bc
-from test_lm_ops_gpu import TYPES, norm_inputs, rnd
+from test_lm_ops_gpu import TYPES, U, norm_inputs, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,26 @@ def test_block_norm_rows_per_gate_is_a_positive_number_read_at_every_call():
         per.fill_(n)
         got = bc.block_norm(r, b, gate=g[:6 // n], rows_per_gate=per).residual_out
         assert torch.equal(got, bc.block_norm(r, b, gate=g[:6 // n].repeat_interleave(n, 0)).residual_out)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [40, 5000, 60000])
+def test_token_logprobs_of_nearly_certain_tokens(vocab, dtype):
+    """One other entry of probability p from 2e-5 to 2e-7: the sum 1 + p is rounded to fp32 (half a step: U), and that
+    is the only rounding of the log probability -log(1 + p) and of the entropy that p's size does not shrink."""
+    rows = 64
+    logits = torch.full((rows, vocab), float("-inf"), device="cuda")
+    logits[:, 7] = 0.0
+    logits[:, 11] = -11.0 - torch.arange(rows, device="cuda") / 16
+    logits = logits.to(dtype)
+    tokens = torch.full((rows,), 7, dtype=torch.int64, device="cuda")
+    got = bc.token_logprobs(logits, tokens, top=2)
+    gap = -logits[:, 11].double()
+    p = (-gap).exp()
+    log_sum = torch.log1p(p)
+    # exp2 is off by 2^-22 and by its argument's rounding (22 U), the last logarithm by 2 steps of its own size
+    slack = 64 * U * p * (1 + gap) + U
+    assert ((got.logprob.double() + log_sum).abs() <= slack).all()
+    assert ((got.lse.double() - log_sum).abs() <= slack).all()
+    assert ((got.top_logprob[:, 0].double() + log_sum).abs() <= slack).all()
+    assert ((got.entropy.double() - (log_sum + p * gap / (1 + p))).abs() <= slack + 2 * U * p * gap).all()
