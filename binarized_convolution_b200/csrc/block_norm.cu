@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
 #include "dtype.cuh"
@@ -456,7 +457,8 @@ __device__ __forceinline__ bool ring_gave_up(const uint32_t* gave_up) {
 }
 // Copies that were issued arrive, so a wait ends.  After a second it gives up all the same: it sets the error word and
 // the CTA's flag, with which no further row is requested or waited for.  (The other copies in flight are as old by
-// then.)  Out of line, it costs the backward no registers (4096 x 4096 bf16 58.1 us, 59.3 with it inline).
+// then.)  Out of line, it costs the 16-bit backward no registers (4096 x 4096 bf16 58.1 us, 59.3 with it inline; fp32
+// 88.3 and 88.1, forward 47.2 and 46.2).
 __device__ __noinline__ void ring_wait_slow(uint64_t* bar, uint32_t parity, uint32_t* gave_up) {
   const uint64_t t0 = tcdev::globaltimer();
   while (!ring_gave_up(gave_up)) {
@@ -1025,27 +1027,46 @@ Shape shape_for(int C, int max_nv) {
 }
 
 // A ring kernel's threads, stages of `stage` bytes and CTAs per SM, of at most `ctas` (what its registers allow),
-// and the bytes of shared memory of a CTA.
+// and the bytes of shared memory of a CTA.  All of these CTAs have to be resident, since each gets its share of the
+// rows: a CTA's static shared memory (below 1 KB) and the 1 KB that the hardware keeps for it count as well, which for
+// narrow rows is much of the SM's 228 KB.  (30000 x 384 bf16 backward with 16 CTAs planned and 15 resident: 70 us.)
 struct Ring {
   int threads, stages, ctas, bytes;
 };
-Ring ring_for(int C, int nv, int stage, int ctas) {
-  Ring r;
+constexpr int kSmBytes = 228 * 1024, kCtaBytes = 2 * 1024;
+constexpr Ring ring_for(int C, int nv, int stage, int ctas) {
+  Ring r{};
   r.threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
-  const int own = 2 * own_weight_bytes(r.threads, nv);
-  r.ctas = std::max(1, std::min(ctas, kRingBytes / (own + 2 * stage)));
-  r.stages = std::max(2, std::min(kMaxRing, (kRingBytes / r.ctas - own) / stage));
+  const int own = 2 * own_weight_bytes(r.threads, nv), least = own + 2 * stage;
+  r.ctas = std::max(1, std::min({ctas, kRingBytes / least, kSmBytes / (least + kCtaBytes)}));
+  const int room = std::min(kRingBytes / r.ctas, kSmBytes / r.ctas - kCtaBytes);
+  r.stages = std::max(2, std::min(kMaxRing, (room - own) / stage));
   r.bytes = own + r.stages * stage;
   return r;
 }
-Ring fwd_ring(int C, int elem) {
+constexpr Ring fwd_ring(int C, int elem) {
   const int nv = elem == 4 ? 1 : 2, threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
   const int ctas = nv == 1 ? 2 * 512 / threads : threads <= 256 ? 3 * 256 / threads : threads <= 384 ? 2 : 1;
   return ring_for(C, nv, 2 * ring_row(C, elem), ctas);
 }
-Ring bwd_ring(int C, int elem) {
+constexpr Ring bwd_ring(int C, int elem) {
   return ring_for(C, kBwdNv, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1);
 }
+constexpr bool resident(const Ring& r) { return r.bytes > kRingBytes || r.ctas * (r.bytes + kCtaBytes) <= kSmBytes; }
+constexpr bool all_resident(int first, int last) {
+  for (int C = first; C <= last; ++C)
+    for (int elem = 2; elem <= 4; elem += 2)
+      if (!resident(fwd_ring(C, elem)) || !resident(bwd_ring(C, elem))) return false;
+  return true;
+}
+template <int I>
+constexpr bool kResident = all_resident(64 * I + 1, 64 * I + 64);  // (in parts: one expression may only be so long)
+template <int... I>
+constexpr bool every_resident(std::integer_sequence<int, I...>) {
+  return (kResident<I + kRingLow / 64> && ...);
+}
+static_assert(every_resident(std::make_integer_sequence<int, (kRingHigh - kRingLow) / 64>()),
+              "every planned CTA has its shared memory");
 
 // Whether a ring of rows of this width has room (two stages fit).
 bool ring_serves(int C, const Ring& r) { return C > kRingLow && C <= kRingHigh && r.bytes <= kRingBytes; }

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import binarized_convolution_b200 as bc
+import test_lm_ops_gpu as gpu
 from test_lm_ops_gpu import TYPES, U, norm_inputs, rnd
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +144,12 @@ def test_token_logprobs_of_nearly_certain_tokens(vocab, dtype):
     assert ((got.lse.double() - log_sum).abs() <= slack).all()
     assert ((got.top_logprob[:, 0].double() + log_sum).abs() <= slack).all()
     assert ((got.entropy.double() - (log_sum + p * gap / (1 + p))).abs() <= slack + 2 * U * p * gap).all()
+
+
+# widths at which the shared memory of the CTAs beside each other is nearly all of it, and where two stages of a row cease to fit
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,per", [(20000, 384, 0), (9000, 800, 1000), (9001, 724, 0), (9000, 840, 500),
+                                            (1200, 5504, 0), (1200, 5536, 0), (1201, 5523, 300), (1100, 7000, 0)])
+def test_block_norm_at_the_edges_of_the_ring(rows, width, per, dtype):
+    gpu.test_block_norm(rows, width, per, dtype)
+    gpu.test_block_norm_backward(rows, width, per, dtype)
