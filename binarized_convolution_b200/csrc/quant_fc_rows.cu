@@ -27,7 +27,15 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxSmem = 100 * 1024;  // of the rows: two CTAs an SM
+constexpr int kMaxSmem = 100 * 1024;  // of the rows: two CTAs an SM, but for the largest calls of 9 to 16 rows
+
+// CTAs that an SM's 228 KB hold: of `smem` bytes for the rows each, the sums of nt tiles of 8 tokens, and the 1 KB that
+// the hardware keeps.
+constexpr int sums_bytes(int nt) { return 2 * kWarps * nt * 4 * 32 * 4; }
+constexpr int ctas_per_sm(int smem, int nt) {
+  return std::max(1, std::min(2, 228 * 1024 / (smem + sums_bytes(nt) + 1024)));
+}
+static_assert(ctas_per_sm(kMaxSmem, 1) == 2 && ctas_per_sm(97 * 1024, 2) == 2 && ctas_per_sm(98 * 1024, 2) == 1, "");
 
 struct RowsArgs {
   QuantFcArgs q;
@@ -71,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) quant_fc_rows_kernel(const RowsAr
   constexpr uint32_t kBias = HALF ? 0x6400u : 0x4300u;  // 1024.0 or 128.0: or-ing a 4-bit number in adds it
   constexpr int kDepth = UNITS == 1 ? 4 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // [part][row][pitch], 256 bytes of zeros
-  __shared__ float sums[2][kWarps][NT * 4][32];  // used in turn, so that one barrier a tile is enough
+  __shared__ float sums[2][kWarps][NT * 4][32];  // sums_bytes(NT); used in turn, so that one barrier a tile is enough
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = static_cast<int>(a.q.rows);
   const int share = warp % a.ksplit, team = warp / a.ksplit, teams = kWarps / a.ksplit;
@@ -318,13 +326,14 @@ cudaError_t launch_quant_fc_rows(const QuantFcArgs& q, int in_dtype, int out_dty
   a.tiles = (q.no + 15) / 16;
   const int smem = smem_for(q, in_dtype);
   const int units = q.group >= kQuantK ? 1 : kQuantK / q.group;
-  // warps per tile: the split that finishes first with two CTAs an SM, a tile's end costing about one step
-  const int slots = 2 * current_sm_count();
+  // warps per tile: the split that finishes first with the CTAs that are resident, the end of a shared tile costing
+  // about one step for every 8 tokens
+  const int nt = q.rows <= 8 ? 1 : 2, slots = ctas_per_sm(smem, nt) * current_sm_count();
   double best = 1e300;
   int ctas = 1;
   for (int ks = 1; ks <= kWarps; ks *= 2) {
     const int teams = kWarps / ks, work = (a.tiles + teams - 1) / teams, each = (q.k_tiles + ks - 1) / ks;
-    const double cost = static_cast<double>((work + slots - 1) / slots) * (each + (ks > 1 ? 1.0 : 0.5));
+    const double cost = static_cast<double>((work + slots - 1) / slots) * (each + (ks > 1 ? nt : 0.5));
     if (cost < best * 0.97) {
       best = cost;
       a.ksplit = ks;

@@ -153,3 +153,12 @@ def test_token_logprobs_of_nearly_certain_tokens(vocab, dtype):
 def test_block_norm_at_the_edges_of_the_ring(rows, width, per, dtype):
     gpu.test_block_norm(rows, width, per, dtype)
     gpu.test_block_norm_backward(rows, width, per, dtype)
+
+
+# calls of 9 to 16 rows whose rows leave room for one CTA on an SM, and their neighbours that leave room for two
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,k,n,group", [(14, 3584, 5000, 128), (13, 3584, 5000, 128), (14, 3400, 20000, 64),
+                                            (15, 3328, 700, 32), (10, 4992, 20000, 128), (9, 5504, 9000, 5504),
+                                            (9, 5505, 300, 128), (12, 4096, 6000, 128)])
+def test_quant_fc_where_one_cta_fits(rows, k, n, group, dtype):
+    gpu.test_quant_fc(rows, k, n, group, dtype)
