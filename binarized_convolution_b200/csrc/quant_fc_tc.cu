@@ -98,18 +98,17 @@ __host__ __device__ constexpr int w_stage_bytes(int units, bool zero) {
   return kQuantTileBytes + (zero ? units * kQuantRows : 0);
 }
 
-// D (+)= A * B^T, A (128 x 16, 16-bit) in TMEM, B (N x 16) in shared memory, fp32 accumulator.  The
+// D += A * B^T, A (128 x 16, 16-bit) in TMEM, B (N x 16) in shared memory, fp32 accumulator.  The
 // descriptor of B (128-byte rows and swizzle) is given by its low word; see smem_desc_sw128.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-template <bool ACCUMULATE>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_desc_low, uint32_t idesc) {
+__device__ __forceinline__ void mma_ts_add(uint32_t d, uint32_t a, uint32_t b_desc_low, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, 1, 0;\n mov.b64 b, {%2, %4};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_desc_low), "r"(idesc), "n"(ACCUMULATE ? 1 : 0), "n"(kDescHigh)
+      "r"(a), "r"(b_desc_low), "r"(idesc), "n"(kDescHigh)
       : "memory");
 }
-// The same where it is known only at run time whether D is added to.
+// The same, or D = A * B^T, as known only at run time.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_desc_low, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
@@ -147,7 +146,6 @@ __device__ __forceinline__ void ld_wait(uint32_t (&v)[16]) {
                : "memory");
 }
 
-// Two 32-bit registers as one of 64 bits, its halves as fp32, and the packed multiply-add on such pairs.
 // Barriers by their shared-memory address: what a single thread does between two MMAs is on the
 // critical path, instruction by instruction.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -374,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = u * kSteps; k < (u + 1) * kSteps; ++k) {
                 const uint32_t b = lo + (k >= kBlockSteps ? desc_block : 0u) + (k % kBlockSteps) * 2u;
                 if (k == u * kSteps) mma_ts(d, a_tmem + k * 8, b, idesc, p > 0);
-                else mma_ts<true>(d, a_tmem + k * 8, b, idesc);
+                else mma_ts_add(d, a_tmem + k * 8, b, idesc);
               }
             }
             commit(full_d + 8 * slot);

@@ -25,10 +25,8 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // active thread and issues the MMA, commit and copy instructions of it, which take warp-uniform
 // operands, directly; behind `lane == 0` each of them became a loop over the active lanes of some 90 cycles.
 __device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0, lane_id = 0;
-  asm volatile(
-      "{\n .reg .b32 r;\n .reg .pred p;\n elect.sync r|p, 0xffffffff;\n @p mov.s32 %0, 1;\n mov.s32 %1, r;\n}\n"
-      : "+r"(pred), "+r"(lane_id));
+  uint32_t pred;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(pred));
   return pred != 0;
 }
 

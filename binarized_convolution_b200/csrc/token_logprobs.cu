@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) token_logprobs_fwd_kernel(con
   now.load(body, threadIdx.x, steps);
   if (has_end) edge[0] = to_f32(row[end_at]);
   uint32_t bound = 0, most = has_end ? order_key(edge[0]) : 0u;  // most: this thread's largest
-  float bound_value = -INFINITY;                                 // (NaN: only NaNs reach it)
+  float bound_value = -INFINITY;                                 // (NaN: every batch is noted)
   if (want) {  // the bound on the top entries, from the threads' first batches
     if (static_cast<int>(threadIdx.x) < steps) most = max(most, order_key(now.largest()));
     bound = bound_of(S, most, top);
