@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import binarized_convolution_b200 as bc
+from binarized_convolution_b200 import lm_ops
 import test_lm_ops_gpu as gpu
 from test_lm_ops_gpu import TYPES, U, norm_inputs, rnd
 
@@ -162,3 +163,34 @@ def test_block_norm_at_the_edges_of_the_ring(rows, width, per, dtype):
                                             (9, 5505, 300, 128), (12, 4096, 6000, 128)])
 def test_quant_fc_where_one_cta_fits(rows, k, n, group, dtype):
     gpu.test_quant_fc(rows, k, n, group, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [37, 4999, 20001])
+def test_token_logprobs_backward_of_views(vocab, dtype):
+    """Gradients whose rows lie otherwise than the logits', from the torch form and with a row stride of their own:
+    the values, and nothing written between the rows."""
+    from binarized_convolution_b200 import _native as nat
+
+    rows, temperature = 6, 0.7
+    base = rnd(vocab, rows, vocab + 21, dtype=dtype, scale=3.0)
+    tokens = torch.tensor([0, 1, -1, 11, vocab // 2, vocab - 1], device="cuda")
+    g, ge = rnd(1, rows), rnd(2, rows)
+    for first in (0, 5, 16):
+        x = base[:, first:first + vocab]
+        f = bc.token_logprobs(x, tokens, temperature=temperature)
+        want, mag = gpu.token_grad_ref(x, tokens, g, ge, temperature)
+        p = (x.double() / temperature).log_softmax(1).exp()
+        # (as for contiguous rows)
+        bound = U * (200 + vocab / 512) * (mag + want.abs()) + p * ge.double().abs()[:, None] / temperature * U * 200 * 12
+        got = bc.token_logprobs_backward(x, tokens, f.lse, f.entropy, d_logprob=g, d_entropy=ge, temperature=temperature)
+        gpu.close(got, want, bound)
+        for shift, stride in ((0, vocab + 3), (1, vocab + 16), (8, vocab + 21), (first, vocab + 21)):
+            wide = torch.full((rows * stride + 32,), 7.0, dtype=dtype, device="cuda")
+            d = wide[shift:shift + rows * stride].view(rows, stride)
+            desc = nat.bconv_token_desc_t(rows, x.stride(0), vocab, lm_ops._DTYPES[dtype], 0, temperature)
+            bc.bconv_token_logprobs_backward(desc, x.data_ptr(), tokens.data_ptr(), f.lse.data_ptr(), f.entropy.data_ptr(),
+                                             g.data_ptr(), ge.data_ptr(), d.data_ptr(), stride,
+                                             torch.cuda.current_stream().cuda_stream)
+            gpu.close(d[:, :vocab], want, bound)
+            assert (d[:, vocab:] == 7).all() and (wide[:shift] == 7).all() and (wide[shift + rows * stride:] == 7).all()
