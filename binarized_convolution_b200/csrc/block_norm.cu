@@ -13,11 +13,12 @@
 // The forward reads two and writes two arrays of rows x C, the backward reads four and writes two, all of
 // them once.  One CTA holds a whole row (its threads 8 channels at a time), so each of the row sums is one block
 // reduction.  Few, narrow or very wide rows take the plain kernels, which hold a row in registers; many rows of
-// 257 to 8192 channels come ahead of their use through a ring in shared memory (below).
+// 257 to 8192 channels (the fp32 backward: to 5500, four arrays being all that two stages have room for) come ahead of
+// their use through a ring in shared memory (below).
 // With many rows HBM is kept 50 to 80 % busy: two reductions a row, each behind a barrier, and as many warps as
-// the registers for sums and rows allow (the backward issues in 58 % of its cycles).  Rows in a graph, us: forward
-// 8192 x 4096 bf16 54, 4096 x 4096 fp32 47 (5.7 TB/s); backward 4096 x 4096 bf16 59, fp32 88 (4.6 TB/s), 8000 x
-// 2001 bf16 90.
+// the registers for sums and rows allow (4096 x 4096 bf16 backward: 128 registers, 15 warps an SM, which issue in 53 % of
+// the cycles).  Rows in a graph, us: forward 8192 x 4096 bf16 53, 4096 x 4096 fp32 47 (5.7 TB/s); backward 4096 x 4096
+// bf16 58, fp32 88 (4.6 TB/s), 8000 x 2001 bf16 61, 30000 x 384 bf16 51.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -1158,8 +1159,10 @@ cudaError_t launch_bwd_ring(const BwdArgs& a, int64_t ctas, cudaStream_t s) {
   return launch_ring<block_norm_bwd_ring_kernel<T, VEC, 512>>(a, ctas, r, s);
 }
 
-// Calls f.operator()<T, NV, VEC, MAX_THREADS> for a row shape; the bound on the threads keeps the
-// registers of the widest rows within what a CTA of that many threads can have.
+// Calls f.operator()<T, NV, VEC, MAX_THREADS> for a row shape.  The bound on the threads is what a CTA's registers are
+// shared out by; the compiler does not use all of them: the backward's instances of 512 threads (8193 to 16384 channels)
+// spill up to 370 bytes of 128 registers, those of 1024 (wider rows) get 32 registers and spill 1.4 to 2.4 KB (2000 x
+// 16384 bf16 218 us, 1000 x 32768 617).
 template <typename T, typename F>
 cudaError_t with_shape(const Shape& sh, bool vec, F&& f) {
   auto pick = [&](auto nv, auto most) {

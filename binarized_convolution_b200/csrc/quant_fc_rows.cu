@@ -12,9 +12,14 @@
 // Warps of a CTA share a channel tile's input channels (ksplit of them) where there are too few
 // tiles to fill the SMs, and add up their sums through shared memory in a fixed order.
 //
-// The codes are all there is to read, but taking them out of their words and biasing them keeps the SMs busy longer than
-// HBM: 1 x 4096 x 65536 bf16 37 us (3.8 TB/s), fp16 35.6 (4.0 TB/s), 1 x 4000 x 65537 fp16 with zeros for groups of 64
-// 46.  The 5th-generation tensor cores would have nothing to gain here: their operands pass through TMEM, one more
+// The rows lie in shared memory as a whole, 100 KB at most: 12 rows of 4096 channels in 16 bits, 4 in fp32; what does
+// not fit takes the tensor-core kernel, one step of which costs more (16 x 4096 -> 16384 bf16 20.9 us, 12 rows 17.6).
+//
+// HBM is not what bounds it: 1 x 4096 x 65536 bf16 38 us (3.7 TB/s), fp16 35.7 (3.9 TB/s), 1 x 4000 x 65537 fp16 with
+// zeros for groups of 64 45.6.  Neither are the issue slots (54 % bf16, 49 % fp16 with groups of 64) nor the integer
+// units that take the codes out of their words (53 %, 41 %) full: the 16 warps an SM wait for one another's results, for
+// codes, and, with small groups, for scales and zeros, of which the ring holds two tiles instead of four.  The
+// 5th-generation tensor cores would have nothing to gain here: their operands pass through TMEM, one more
 // step for every code (with that kernel 68, 66 and 76 us, its MMAs idle most of the time).
 #include <algorithm>
 #include <type_traits>

@@ -30,8 +30,11 @@
 // the input channels: 44 of 140 us for 2000 x 4096 x 8192).  Where there are few tiles, a cluster of CTAs
 // shares a tile's input channels and adds up its parts over distributed shared memory in rank order.
 //
-// Bound by HBM (the codes) for few tokens and by the tensor cores (4 N cycles per 128 input channels)
-// for many; groups of 32 and 64 are bound by taking out their sums.
+// No unit is full.  For many tokens the tensor cores (4 N cycles per 128 input channels) are busy most (2000 x 4096 ->
+// 8192 bf16: 55 %, issue slots 52 %; 160 x 4096 -> 16384: 41 % and 47 %), for few the chain of decoding a tile, its MMAs
+// and taking out their sums is (9 x 25088 -> 4096 fp32: tensor cores 10 %, issue slots 40 %, HBM 19 %); warps wait most
+// for loads, those from TMEM among them.  Groups of 32 and 64 have two and four times as many sums to take out, fp32 rows
+// above 32 three times the MMAs on at most 64 tokens (160 x 4096 -> 16384 fp32 81 us, 2000 x 4096 -> 8192 374).
 // Every wait gives up after one second, sets the error word and makes all roles stop.
 #include <cuda.h>
 #include <cudaTypedefs.h>

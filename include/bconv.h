@@ -411,7 +411,7 @@ int64_t bfc_quant_workspace_bytes(bfc_quant_handle_t h, const void* in, int64_t 
  * in (device, row r at in + r * in_stride elements, in_channels each) -> out (device, row
  * stride out_stride).  workspace: device, 256-byte aligned, of bfc_quant_workspace_bytes(h, in,
  * in_stride, rows) bytes (NULL when that is 0), used until the work on `stream` completes.  Elements between a
- * row's end and its stride are neither read nor written.  Errors: INVALID_ARG (also strides
+ * row's end and its stride are neither read nor written; out must not overlap in.  Errors: INVALID_ARG (also strides
  * below the channel counts, rows < 0 or above 2^24, a missing or misaligned workspace), CUDA.
  */
 bconv_status_t bfc_quant_forward(bfc_quant_handle_t h, const void* in, int64_t in_stride, int64_t rows, void* out,
