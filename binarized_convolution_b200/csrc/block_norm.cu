@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "dtype.cuh"
+#include "elect.cuh"
 #include "f32x2.cuh"
 #include "host_util.cuh"
 #include "tc_device.cuh"
@@ -1035,9 +1036,11 @@ struct Ring {
   int threads, stages, ctas, bytes;
 };
 constexpr int kSmBytes = 228 * 1024, kCtaBytes = 2 * 1024;
+// Threads, in whole warps, for C channels in vectors of 8, nv of them a thread.
+constexpr int ring_threads(int C, int nv) { return (C + 8 * nv * 32 - 1) / (8 * nv * 32) * 32; }
 constexpr Ring ring_for(int C, int nv, int stage, int ctas) {
   Ring r{};
-  r.threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
+  r.threads = ring_threads(C, nv);
   const int own = 2 * own_weight_bytes(r.threads, nv), least = own + 2 * stage;
   r.ctas = std::max(1, std::min({ctas, kRingBytes / least, kSmBytes / (least + kCtaBytes)}));
   const int room = std::min(kRingBytes / r.ctas, kSmBytes / r.ctas - kCtaBytes);
@@ -1046,12 +1049,12 @@ constexpr Ring ring_for(int C, int nv, int stage, int ctas) {
   return r;
 }
 constexpr Ring fwd_ring(int C, int elem) {
-  const int nv = elem == 4 ? 1 : 2, threads = round_up((C + 8 * nv - 1) / (8 * nv), 32);
+  const int nv = elem == 4 ? 1 : 2, threads = ring_threads(C, nv);
   const int ctas = nv == 1 ? 2 * 512 / threads : threads <= 256 ? 3 * 256 / threads : threads <= 384 ? 2 : 1;
   return ring_for(C, nv, 2 * ring_row(C, elem), ctas);
 }
 constexpr Ring bwd_ring(int C, int elem) {
-  return ring_for(C, kBwdNv, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / round_up((C + 15) / 16, 32) : 1);
+  return ring_for(C, kBwdNv, 4 * ring_row(C, elem), C <= 4096 ? 2 * 256 / ring_threads(C, kBwdNv) : 1);
 }
 constexpr bool resident(const Ring& r) { return r.bytes > kRingBytes || r.ctas * (r.bytes + kCtaBytes) <= kSmBytes; }
 constexpr bool all_resident(int first, int last) {

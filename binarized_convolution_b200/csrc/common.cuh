@@ -26,7 +26,7 @@ constexpr int kWordBits = 32;
 constexpr int kWordPad = 8;
 
 inline int words_for(int bits) { return (bits + kWordBits - 1) / kWordBits; }
-constexpr int round_up(int v, int m) { return (v + m - 1) / m * m; }
+inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Multiprocessor count of the current device (cached per device).

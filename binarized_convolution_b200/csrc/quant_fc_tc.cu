@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "elect.cuh"
 #include "f32x2.cuh"
 #include "host_util.cuh"
 #include "quant_fc.cuh"

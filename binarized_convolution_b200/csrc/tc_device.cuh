@@ -21,15 +21,6 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
-// True in one lane of the (converged) warp.  The compiler knows that a region behind this has one
-// active thread and issues the MMA, commit and copy instructions of it, which take warp-uniform
-// operands, directly; behind `lane == 0` each of them became a loop over the active lanes of some 90 cycles.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(pred));
-  return pred != 0;
-}
-
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
 }
